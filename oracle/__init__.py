@@ -30,3 +30,4 @@ from .dspark_schedule_oracle import (  # noqa: F401
     schedule_prefix,
     expected_tokens,
 )
+from . import serve_oracle  # noqa: F401

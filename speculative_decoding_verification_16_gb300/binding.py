@@ -367,3 +367,279 @@ def spec_verify_shard_finish(cands, merged, verify_lens, row_offsets, *, out: Ou
             _ptr(cands), _i32(world), _ptr(merged), _ptr(verify_lens), _ptr(row_offsets),
             _ptr(out.accept_len), _i32(B), _i32(out.tokens.numel()), _ptr(out.tokens),
             _ptr(out.dev_error), _stream_of(cands, stream)))
+
+
+# ---- the paged serving operators around the verify step
+#      (include/spec_verify_serve.h)
+
+SV_DEVERR_PARAM, SV_DEVERR_BLOCKS, SV_DEVERR_PAGE = 16, 32, 64
+SV_SAMPLE_MAX_ROW_BYTES = 1572864
+SV_SLOTS_MAX_B = 8192
+SV_ATTN_MAX_HEAD_DIM = 256
+_i64 = ctypes.c_int64
+_lib.spec_verify_sample.argtypes = [_vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                    _vp, _vp, _vp]
+_lib.spec_verify_slots.argtypes = [_vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _vp,
+                                   _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.spec_verify_append.argtypes = [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _i32, _i32, _i32, _vp,
+                                    _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _vp]
+_lib.spec_verify_attention.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64,
+                                       _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                       _i32, _i32, _f32, _i32, _vp, _i64, _i64, _vp, _vp, _vp,
+                                       _sz, _vp]
+_lib.spec_verify_attention_workspace_size.argtypes = [_i32, _i32, _i32, _i32]
+_lib.spec_verify_attention_workspace_size.restype = ctypes.c_size_t
+for _name in ("spec_verify_sample", "spec_verify_slots", "spec_verify_append",
+              "spec_verify_attention"):
+    getattr(_lib, _name).restype = ctypes.c_int
+_DTYPES = {torch.bfloat16: SV_BF16, torch.float32: SV_FP32}
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _issue(fn, device, stream, *args):
+    """Call one entry point on `stream` (None: the device's current one) with
+    the tensors' device current, as the C ABI requires."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    else:
+        rc = fn(*args, stream.cuda_stream)
+    if rc != SV_OK:
+        raise SpecVerifyError(rc)
+
+
+def _new(shape, dtype, device, stream, zero=False):
+    """A tensor that the call itself allocates, on the stream that uses it."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _expect(name, t, dtype, shape, device):
+    """A contiguous tensor of this dtype and shape on this device (None passes)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {shape}, "
+                         f"got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _rows_of_heads(name, t, dtype, device):
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [rows, heads, head_dim] with a contiguous last dimension")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _caches(key_cache, value_cache, kv_heads, head_dim, dtype, device):
+    """The strides that both caches share."""
+    for name, c in (("key_cache", key_cache), ("value_cache", value_cache)):
+        if c.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {c.dtype}")
+        if c.dim() != 4 or (head_dim > 1 and c.stride(3) != 1):
+            raise ValueError(f"{name} must be [num_blocks, page_size, kv_heads, head_dim] with a "
+                             "contiguous last dimension")
+        if c.device != device:
+            raise ValueError(f"{name} is on {c.device}, expected {device}")
+    if key_cache.shape != value_cache.shape or key_cache.stride() != value_cache.stride():
+        raise ValueError("key_cache and value_cache must have the same shape and strides")
+    if kv_heads is not None and key_cache.shape[2] != kv_heads:
+        raise ValueError(f"the caches hold {key_cache.shape[2]} heads, expected {kv_heads}")
+    if key_cache.shape[3] != head_dim:
+        raise ValueError(f"the caches' head_dim is {key_cache.shape[3]}, expected {head_dim}")
+    return key_cache.stride()
+
+
+def spec_verify_sample(logits, uniforms, *, temperature=None, top_k=None, top_p=None, min_p=None,
+                       out_tokens=None, out_probs=None, want_probs=False, dev_error=None,
+                       stream=None):
+    """One token per row of ``logits`` [N, V] (bf16 or fp32, rows at any
+    stride) from its uniform number in [0, 1): temperature, then top_k, top_p
+    and min_p, each a [N] tensor or None (1, off, off, off); temperature 0 is
+    the argmax.  Returns (tokens int32 [N], probs float32 [N] or None: the
+    token's probability in the kept set)."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [N, V] with contiguous rows")
+    if logits.dtype not in _DTYPES:
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    (N, V), dev = logits.shape, logits.device
+    _expect("uniforms", uniforms, torch.float32, (N,), dev)
+    _expect("temperature", temperature, torch.float32, (N,), dev)
+    _expect("top_k", top_k, torch.int32, (N,), dev)
+    _expect("top_p", top_p, torch.float32, (N,), dev)
+    _expect("min_p", min_p, torch.float32, (N,), dev)
+    _expect("out_tokens", out_tokens, torch.int32, (N,), dev)
+    _expect("out_probs", out_probs, torch.float32, (N,), dev)
+    _expect("dev_error", dev_error, torch.int32, (1,), dev)
+    if out_tokens is None:
+        out_tokens = _new(N, torch.int32, dev, stream)
+    if out_probs is None and want_probs:
+        out_probs = _new(N, torch.float32, dev, stream)
+    _issue(_lib.spec_verify_sample, dev, stream, logits.data_ptr(),
+           max(logits.stride(0), V) if N < 2 else logits.stride(0), N, V, _DTYPES[logits.dtype],
+           _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p), uniforms.data_ptr(),
+           out_tokens.data_ptr(), _addr(out_probs), _addr(dev_error))
+    return out_tokens, out_probs
+
+
+class SlotOutputs:
+    """Device outputs of spec_verify_slots."""
+
+    def __init__(self, row_offsets, seq_lens, positions, slots, held, free_count):
+        self.row_offsets = row_offsets
+        self.seq_lens = seq_lens
+        self.positions = positions
+        self.slots = slots
+        self.held = held
+        self.free_count = free_count
+
+
+def spec_verify_slots(context_lens, verify_lens, block_table, held, free_list, free_count, *,
+                      page_size, n_rows=None, row_offsets=None, seq_lens=None, positions=None,
+                      slots=None, held_out=None, free_count_out=None, dev_error=None, stream=None):
+    """Block tables and slot maps of a step.  ``block_table`` [B, width] and
+    ``free_list`` are updated in place so that every request holds exactly the
+    pages of its context and new tokens; ``held`` [B] and ``free_count`` [1]
+    are the counts before the call and are returned anew (``held_out`` and
+    ``free_count_out`` must be other tensors).  Returns SlotOutputs: prefix
+    sums of verify_lens [B + 1], sequence lengths [B], and for ``n_rows`` rows
+    (at least the sum of verify_lens; the length of ``slots`` if given) the
+    positions int32 and slots int64."""
+    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [B, width] with contiguous rows")
+    (B, width), dev = block_table.shape, block_table.device
+    if block_table.dtype != torch.int32:
+        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
+    if n_rows is None:
+        if slots is None:
+            raise ValueError("n_rows is needed where slots is not given")
+        n_rows = slots.numel()
+    i32 = torch.int32
+    _expect("context_lens", context_lens, i32, (B,), dev)
+    _expect("verify_lens", verify_lens, i32, (B,), dev)
+    _expect("held", held, i32, (B,), dev)
+    _expect("free_list", free_list, i32, (free_list.numel(),), dev)
+    _expect("free_count", free_count, i32, (1,), dev)
+    _expect("row_offsets", row_offsets, i32, (B + 1,), dev)
+    _expect("seq_lens", seq_lens, i32, (B,), dev)
+    _expect("positions", positions, i32, (n_rows,), dev)
+    _expect("slots", slots, torch.int64, (n_rows,), dev)
+    _expect("held_out", held_out, i32, (B,), dev)
+    _expect("free_count_out", free_count_out, i32, (1,), dev)
+    _expect("dev_error", dev_error, i32, (1,), dev)
+    if row_offsets is None:
+        row_offsets = _new(B + 1, i32, dev, stream)
+    if seq_lens is None:
+        seq_lens = _new(B, i32, dev, stream)
+    if positions is None:
+        positions = _new(n_rows, i32, dev, stream)
+    if slots is None:
+        slots = _new(n_rows, torch.int64, dev, stream)
+    if held_out is None:
+        held_out = _new(B, i32, dev, stream)
+    if free_count_out is None:
+        free_count_out = _new(1, i32, dev, stream)
+    _issue(_lib.spec_verify_slots, dev, stream, context_lens.data_ptr(), verify_lens.data_ptr(),
+           B, page_size, block_table.data_ptr(),
+           max(block_table.stride(0), width) if B < 2 else block_table.stride(0), width,
+           held.data_ptr(), free_list.data_ptr(), free_list.numel(), free_count.data_ptr(), n_rows,
+           row_offsets.data_ptr(), seq_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+           held_out.data_ptr(), free_count_out.data_ptr(), _addr(dev_error))
+    return SlotOutputs(row_offsets, seq_lens, positions, slots, held_out, free_count_out)
+
+
+def spec_verify_append(key, value, slots, key_cache, value_cache, *, dev_error=None, stream=None):
+    """Write ``key`` and ``value`` [n_rows, kv_heads, head_dim] (any row and
+    head strides, e.g. slices of a fused projection) to their slots of the
+    caches [num_blocks, page_size, kv_heads, head_dim] (any strides; a cache
+    laid out [num_blocks, kv_heads, page_size, head_dim] is passed transposed).
+    Negative slots are skipped."""
+    dev, dtype = key_cache.device, key_cache.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"the caches must be bfloat16 or float32, got {dtype}")
+    _rows_of_heads("key", key, dtype, dev)
+    _rows_of_heads("value", value, dtype, dev)
+    if key.shape != value.shape:
+        raise ValueError("key and value must have the same shape")
+    N, H, D = key.shape
+    sb, st, sh, _ = _caches(key_cache, value_cache, H, D, dtype, dev)
+    _expect("slots", slots, torch.int64, (N,), dev)
+    _expect("dev_error", dev_error, torch.int32, (1,), dev)
+    _issue(_lib.spec_verify_append, dev, stream, key.data_ptr(), value.data_ptr(), key.stride(0),
+           key.stride(1), value.stride(0), value.stride(1), slots.data_ptr(), N, H, D,
+           key_cache.data_ptr(), value_cache.data_ptr(), sb, st, sh, key_cache.shape[0],
+           key_cache.shape[1], _DTYPES[dtype], _addr(dev_error))
+
+
+def spec_verify_attention_workspace_size(n_rows, heads, head_dim, dtype=torch.bfloat16) -> int:
+    return int(_lib.spec_verify_attention_workspace_size(int(n_rows), int(heads), int(head_dim),
+                                                         _DTYPES[dtype]))
+
+
+def alloc_attention_workspace(query) -> torch.Tensor:
+    """Device workspace of spec_verify_attention for queries of this shape."""
+    return torch.empty(spec_verify_attention_workspace_size(*query.shape, query.dtype),
+                       dtype=torch.uint8, device=query.device)
+
+
+def spec_verify_attention(query, key_cache, value_cache, block_table, seq_lens, row_offsets, *,
+                          max_len, scale=None, window=0, out=None, lse=None, want_lse=False,
+                          workspace=None, dev_error=None, stream=None):
+    """Attention of every request's new tokens (rows row_offsets[r] ..
+    row_offsets[r+1] - 1 of ``query`` [n_rows, heads, head_dim], the last of its
+    seq_lens[r] tokens) over its pages of the caches, causal within the chunk;
+    ``window`` > 0 keeps the last window keys of each row; ``scale`` defaults to
+    head_dim ** -0.5; ``max_len`` is a host upper bound of the new tokens of a
+    request.  Returns (out, lse or None)."""
+    dev, dtype = query.device, query.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"query must be bfloat16 or float32, got {dtype}")
+    _rows_of_heads("query", query, dtype, dev)
+    N, H, D = query.shape
+    sb, st, sh, _ = _caches(key_cache, value_cache, None, D, dtype, dev)
+    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [B, width] with contiguous rows")
+    if block_table.dtype != torch.int32:
+        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
+    if block_table.device != dev:
+        raise ValueError(f"block_table is on {block_table.device}, expected {dev}")
+    B, width = block_table.shape
+    _expect("seq_lens", seq_lens, torch.int32, (B,), dev)
+    _expect("row_offsets", row_offsets, torch.int32, (B + 1,), dev)
+    _expect("lse", lse, torch.float32, (N, H), dev)
+    _expect("dev_error", dev_error, torch.int32, (1,), dev)
+    if out is None:
+        out = _new((N, H, D), dtype, dev, stream)
+    else:
+        _rows_of_heads("out", out, dtype, dev)
+        if out.shape != query.shape:
+            raise ValueError("out must have the query's shape")
+    if lse is None and want_lse:
+        lse = _new((N, H), torch.float32, dev, stream)
+    if workspace is None:
+        workspace = _new(spec_verify_attention_workspace_size(N, H, D, dtype), torch.uint8, dev,
+                         stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    _issue(_lib.spec_verify_attention, dev, stream, query.data_ptr(), query.stride(0),
+           query.stride(1), key_cache.data_ptr(), value_cache.data_ptr(), sb, st, sh,
+           block_table.data_ptr(), max(block_table.stride(0), width) if B < 2 else
+           block_table.stride(0), width, seq_lens.data_ptr(), row_offsets.data_ptr(), B, N,
+           max_len, H, key_cache.shape[2], D, key_cache.shape[0], key_cache.shape[1],
+           _DTYPES[dtype], D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+           out.stride(0), out.stride(1), _addr(lse), _addr(dev_error), workspace.data_ptr(),
+           workspace.numel() * workspace.element_size())
+    return out, lse

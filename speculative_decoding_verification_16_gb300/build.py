@@ -1,8 +1,9 @@
 """Build step of the C-ABI library ``libspecverify.so`` (sm_103a).
 
-Two translation units (the verify step, and its vocabulary-sharded form),
-one ``-gencode``, compiled in-tree next to this file with ``nvcc -shared``.  Rebuilds only when a source or the header is newer
-than the library.
+One translation unit each for the verify step, its vocabulary-sharded form,
+slot maps and cache writes, sampling, and paged attention; one ``-gencode``,
+compiled in parallel, in-tree next to this file, with ``nvcc -shared``.
+Rebuilds only when a source or a header is newer than the library.
 """
 
 from __future__ import annotations
@@ -16,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libspecverify.so")
-SOURCES = [os.path.join(CSRC, "spec_verify.cu"), os.path.join(CSRC, "sv_shard.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "sv_shard.cu", "sv_slots.cu",
+                                           "sv_sample.cu", "sv_attention.cu")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -39,7 +41,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         t = os.path.getmtime(LIB)
         if all(os.path.getmtime(f) <= t for f in _deps()):
             return LIB
-    cmd = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
+    cmd = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "--threads", "0",
            "-Xcompiler", "-fPIC", "-Xptxas", "-v" if verbose else "-O3",
            "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", LIB + ".tmp", "-lcudart"]
     res = subprocess.run(cmd, capture_output=True, text=True)

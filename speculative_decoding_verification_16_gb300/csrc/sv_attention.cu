@@ -1,0 +1,209 @@
+// sv_attention.cu -- attention of a chunk of new tokens over a paged cache
+// (include/spec_verify_serve.h).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "sv_host.cuh"
+#include "sv_ptx.cuh"
+
+namespace sv {
+namespace serve {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kInf = __builtin_huge_valf();
+
+struct AttnArgs {
+  const char* q;
+  int64_t q_row, q_head;  // bytes
+  const char *k, *v;
+  int64_t block, token, head;  // bytes
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t table_width;
+  const int32_t *seq_lens, *row_offsets;
+  int32_t B, n_rows, max_len, heads, group, dim, num_blocks, page, window;
+  float scale2;  // scale * log2(e): scores in powers of two
+  char* out;
+  int64_t o_row, o_head;  // bytes
+  float* lse;
+  int32_t* dev_error;
+};
+
+// Request r's rows and length, or l = -1 when they are out of range.
+struct Span {
+  int32_t row0, l, seq;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int r) {
+  Span s;
+  s.row0 = a.row_offsets[r];
+  const int32_t end = a.row_offsets[r + 1];
+  s.seq = a.seq_lens[r];
+  const bool ok = s.row0 >= 0 && end >= s.row0 && end <= a.n_rows && end - s.row0 <= a.max_len &&
+                  s.seq >= 0 && s.seq <= static_cast<int64_t>(a.table_width) * a.page;
+  s.l = ok ? end - s.row0 : -1;
+  return s;
+}
+
+// ---------------------------------------------------------------- fp32
+//
+// One warp a (row, head): 32 keys at a time, a lane its own key's score, then
+// the lanes own the head's dimensions for the weighted sum of the values.
+constexpr int kRowWarps = 4;
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
+
+template <typename T>
+__global__ __launch_bounds__(kRowWarps * 32) void attn_rows_kernel(const AttnArgs a) {
+  __shared__ float qs[kRowWarps][SV_ATTN_MAX_HEAD_DIM];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
+  const int row = static_cast<int>(item / a.heads), h = static_cast<int>(item % a.heads);
+  if (row >= a.n_rows) return;
+  int lo = 0, hi = a.B;  // the request: last r with row_offsets[r] <= row
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.row_offsets[mid] <= row) lo = mid; else hi = mid;
+  }
+  const Span s = span_of(a, lo);
+  if (s.l < 0) {
+    if (lane == 0 && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_LEN);
+    return;
+  }
+  if (row < s.row0 || row >= s.row0 + s.l) return;
+  const T* q = reinterpret_cast<const T*>(a.q + row * a.q_row + h * a.q_head);
+  for (int d = lane; d < a.dim; d += 32) qs[warp][d] = to_float(q[d]);
+  __syncwarp();
+  const int pos = s.seq - s.l + row - s.row0;
+  const int first = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+  const int64_t hoff = (h / a.group) * a.head;
+  constexpr int kPer = SV_ATTN_MAX_HEAD_DIM / 32;
+  float m = -kInf, z = 0, o[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = 0;
+  for (int t0 = first; t0 <= pos; t0 += 32) {
+    const int t = t0 + lane;
+    int64_t at = 0;
+    float x = -kInf;
+    if (t <= pos) {
+      int id = a.table[lo * a.table_stride + t / a.page];
+      if (id < 0 || id >= a.num_blocks) {
+        if (a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_PAGE);
+        id = 0;
+      }
+      at = id * a.block + (t % a.page) * a.token + hoff;
+      const T* k = reinterpret_cast<const T*>(a.k + at);
+      float dot = 0;
+      for (int d = 0; d < a.dim; ++d) dot = fmaf(qs[warp][d], to_float(k[d]), dot);
+      x = dot * a.scale2;
+    }
+    float top = x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    const float next = fmaxf(m, top);
+    const float base = next == -kInf ? 0.0f : next;
+    const float p = ex2(x - base), keep = ex2(m - base);
+    float sum = p;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    z = z * keep + sum;
+    m = next;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] *= keep;
+    const int n = min(32, pos - t0 + 1);
+    for (int j = 0; j < n; ++j) {
+      const float pj = __shfl_sync(~0u, p, j);
+      const T* v = reinterpret_cast<const T*>(a.v + __shfl_sync(~0u, at, j));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i * 32 + lane < a.dim) o[i] = fmaf(pj, to_float(v[i * 32 + lane]), o[i]);
+    }
+  }
+  T* out = reinterpret_cast<T*>(a.out + row * a.o_row + h * a.o_head);
+  const bool none = pos < 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (i * 32 + lane < a.dim) out[i * 32 + lane] = from_float<T>(none ? 0.0f : o[i] / z);
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[static_cast<int64_t>(row) * a.heads + h] = none ? -kInf : (m + log2f(z)) * kLn2;
+}
+
+}  // namespace
+}  // namespace serve
+}  // namespace sv
+
+extern "C" {
+
+size_t spec_verify_attention_workspace_size(int32_t n_rows, int32_t heads, int32_t head_dim,
+                                            int32_t dtype) {
+  (void)n_rows, (void)heads, (void)head_dim, (void)dtype;
+  return 256;
+}
+
+int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_head_stride,
+                          const void* key_cache, const void* value_cache, int64_t block_stride,
+                          int64_t token_stride, int64_t head_stride, const int32_t* block_table,
+                          int64_t table_stride, int32_t table_width, const int32_t* seq_lens,
+                          const int32_t* row_offsets, int32_t B, int32_t n_rows, int32_t max_len,
+                          int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t num_blocks,
+                          int32_t page_size, int32_t dtype, float scale, int32_t window,
+                          void* out, int64_t o_row_stride, int64_t o_head_stride, float* out_lse,
+                          int32_t* dev_error, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  using namespace sv::serve;
+  if (dtype != SV_BF16 && dtype != SV_FP32) return SV_ERR_DTYPE;
+  const int es = dtype == SV_BF16 ? 2 : 4;
+  if (B < 1 || n_rows < 0 || max_len < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
+      head_dim < 1 || num_blocks < 1 || page_size < 1 || table_width < 1 ||
+      table_stride < table_width || !std::isfinite(scale))
+    return SV_ERR_ARG;
+  if (head_dim % 8 != 0 || head_dim > SV_ATTN_MAX_HEAD_DIM) return SV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(table_width) * page_size > INT32_MAX / 2 ||
+      static_cast<int64_t>(n_rows) * heads > INT32_MAX)
+    return SV_ERR_UNSUPPORTED;
+  if (query == nullptr || key_cache == nullptr || value_cache == nullptr || out == nullptr ||
+      block_table == nullptr || seq_lens == nullptr || row_offsets == nullptr)
+    return SV_ERR_ARG;
+  for (const void* p : {query, key_cache, value_cache, static_cast<const void*>(out)})
+    if (!aligned_to(p, 16)) return SV_ERR_ARG;
+  for (int64_t s : {q_row_stride, q_head_stride, block_stride, token_stride, head_stride,
+                    o_row_stride, o_head_stride})
+    if (s < 0 || s * es % 16 != 0) return SV_ERR_ARG;
+  if (!aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(row_offsets, 4) ||
+      !null_or_aligned(out_lse, 4) || !null_or_aligned(dev_error, 4))
+    return SV_ERR_ARG;
+  if (workspace == nullptr || !aligned_to(workspace, 256) ||
+      workspace_bytes < spec_verify_attention_workspace_size(n_rows, heads, head_dim, dtype))
+    return SV_ERR_WORKSPACE;
+  if (n_rows == 0) return SV_OK;
+  const AttnArgs a{static_cast<const char*>(query), q_row_stride * es, q_head_stride * es,
+                   static_cast<const char*>(key_cache), static_cast<const char*>(value_cache),
+                   block_stride * es, token_stride * es, head_stride * es, block_table,
+                   table_stride, table_width, seq_lens, row_offsets, B, n_rows, max_len, heads,
+                   heads / kv_heads, head_dim, num_blocks, page_size, window, scale * kLog2e,
+                   static_cast<char*>(out), o_row_stride * es, o_head_stride * es, out_lse,
+                   dev_error};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t items = static_cast<int64_t>(n_rows) * heads;
+  const dim3 grid(static_cast<unsigned>((items + kRowWarps - 1) / kRowWarps));
+  return es == 2 ? launch(attn_rows_kernel<__nv_bfloat16>, grid, kRowWarps * 32, 0, 1, false, st, a)
+                 : launch(attn_rows_kernel<float>, grid, kRowWarps * 32, 0, 1, false, st, a);
+}
+
+}  // extern "C"
