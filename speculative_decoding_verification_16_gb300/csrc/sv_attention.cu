@@ -12,7 +12,6 @@
 
 namespace sv {
 namespace serve {
-namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -144,6 +143,108 @@ __global__ __launch_bounds__(kRowWarps * 32) void attn_rows_kernel(const AttnArg
     a.lse[static_cast<int64_t>(row) * a.heads + h] = none ? -kInf : (m + log2f(z)) * kLn2;
 }
 
+}  // namespace serve
+}  // namespace sv
+
+#include "sv_attn_mma.cuh"
+
+namespace sv {
+namespace serve {
+namespace {
+
+constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+constexpr size_t kRecordBytes = round256(sizeof(AttnRecord) * kMaxWorkers);
+constexpr size_t kMlBytes = sizeof(float2) * 2 * kMaxWorkers * kTile;
+
+bool on_tensor_cores(int dtype, int head_dim) { return dtype == SV_BF16 && head_dim <= 128; }
+
+size_t workspace_bytes_of(int dtype, int head_dim) {
+  if (!on_tensor_cores(dtype, head_dim)) return 256;
+  const size_t dp = head_dim <= 64 ? 64 : 128;
+  return kRecordBytes + kMlBytes + sizeof(float) * 2 * kMaxWorkers * kTile * dp;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// A cache as (head_dim, token of a page, head, page), copied in boxes of 64
+// columns and `box` tokens.
+bool encode_cache(CUtensorMap* map, const void* base, const AttnArgs& a, int kv_heads, int box) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.page),
+                              static_cast<cuuint64_t>(kv_heads),
+                              static_cast<cuuint64_t>(a.num_blocks)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.token), static_cast<cuuint64_t>(a.head),
+                           static_cast<cuuint64_t>(a.block)};
+  for (int i = 0; i < 3; ++i)
+    if (dims[i + 1] == 1) strides[i] = 16;  // never stepped along
+  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, one[4] = {1, 1, 1, 1};
+  const EncodeTiled fn = encode_tiled();
+  return fn != nullptr &&
+         fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NS, int DP>
+int launch_mma(const MmaArgs& p, int grid, const CUtensorMap& km, const CUtensorMap& vm,
+               cudaStream_t st) {
+  constexpr int threads = (NS * 4 + 2) * 32, smem = attn_smem(NS, DP);
+  int rc = p.box > 0
+               ? launch(attn_mma_kernel<NS, DP, true>, dim3(grid), threads, smem, 1, false, st, p, km, vm)
+               : launch(attn_mma_kernel<NS, DP, false>, dim3(grid), threads, smem, 1, false, st, p, km, vm);
+  if (rc != SV_OK || grid == 1) return rc;  // one worker cuts no item
+  return launch(attn_combine_kernel<NS * kTile, DP>, dim3(grid, NS * kTile / kCombineRows),
+                kCombineThreads, 0, 1, true, st, p);
+}
+
+int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
+  Device d;
+  const int rc = device(&d);
+  if (rc != SV_OK) return rc;
+  const int dp = a.dim <= 64 ? 64 : 128;
+  char* ws = static_cast<char*>(workspace);
+  MmaArgs p{a, kv_heads, 0, reinterpret_cast<AttnRecord*>(ws),
+            reinterpret_cast<float2*>(ws + kRecordBytes),
+            reinterpret_cast<float4*>(ws + kRecordBytes + kMlBytes)};
+  // whole page pieces by tensor copies where pages hold a number of them and
+  // the strides fit a tensor map
+  p.box = a.page % 64 == 0 ? 64 : a.page == 8 || a.page == 16 || a.page == 32 ? a.page : 0;
+  for (int64_t s : {a.block, a.token, a.head})
+    if (s >= (int64_t{1} << 40)) p.box = 0;
+  if ((a.block == 0 && a.num_blocks > 1) || (a.token == 0 && a.page > 1) ||
+      (a.head == 0 && kv_heads > 1))
+    p.box = 0;
+  CUtensorMap km{}, vm{};
+  if (p.box > 0 && (!encode_cache(&km, a.k, a, kv_heads, p.box) ||
+                    !encode_cache(&vm, a.v, a, kv_heads, p.box)))
+    return SV_ERR_CUDA;
+  const int64_t rows = std::min<int64_t>(a.max_len, a.n_rows) * a.group;
+  const int ns = rows > kTile ? 2 : 1;
+  const int64_t keys = static_cast<int64_t>(a.table_width) * a.page;
+  const int64_t tiles = (rows + ns * kTile - 1) / (ns * kTile) * ((keys + kTile - 1) / kTile) *
+                        a.B * kv_heads;
+  const int64_t most = ns == 1 ? std::min(2 * d.sms, kMaxWorkers) : std::min(d.sms, kMaxWorkers / 2);
+  const int grid = static_cast<int>(std::min(most, tiles));
+  if (ns == 1)
+    return dp == 64 ? launch_mma<1, 64>(p, grid, km, vm, st) : launch_mma<1, 128>(p, grid, km, vm, st);
+  return dp == 64 ? launch_mma<2, 64>(p, grid, km, vm, st) : launch_mma<2, 128>(p, grid, km, vm, st);
+}
+
 }  // namespace
 }  // namespace serve
 }  // namespace sv
@@ -152,8 +253,8 @@ extern "C" {
 
 size_t spec_verify_attention_workspace_size(int32_t n_rows, int32_t heads, int32_t head_dim,
                                             int32_t dtype) {
-  (void)n_rows, (void)heads, (void)head_dim, (void)dtype;
-  return 256;
+  (void)n_rows, (void)heads;
+  return sv::serve::workspace_bytes_of(dtype, head_dim);
 }
 
 int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_head_stride,
@@ -182,8 +283,11 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
     return SV_ERR_ARG;
   for (const void* p : {query, key_cache, value_cache, static_cast<const void*>(out)})
     if (!aligned_to(p, 16)) return SV_ERR_ARG;
-  for (int64_t s : {q_row_stride, q_head_stride, block_stride, token_stride, head_stride,
-                    o_row_stride, o_head_stride})
+  // a dimension of one is never stepped along, whatever its stride says
+  for (int64_t s : {n_rows > 1 ? q_row_stride : 0, heads > 1 ? q_head_stride : 0,
+                    num_blocks > 1 ? block_stride : 0, page_size > 1 ? token_stride : 0,
+                    kv_heads > 1 ? head_stride : 0, n_rows > 1 ? o_row_stride : 0,
+                    heads > 1 ? o_head_stride : 0})
     if (s < 0 || s * es % 16 != 0) return SV_ERR_ARG;
   if (!aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(row_offsets, 4) ||
       !null_or_aligned(out_lse, 4) || !null_or_aligned(dev_error, 4))
@@ -192,14 +296,17 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
       workspace_bytes < spec_verify_attention_workspace_size(n_rows, heads, head_dim, dtype))
     return SV_ERR_WORKSPACE;
   if (n_rows == 0) return SV_OK;
+  const float c = scale * kLog2e;
   const AttnArgs a{static_cast<const char*>(query), q_row_stride * es, q_head_stride * es,
                    static_cast<const char*>(key_cache), static_cast<const char*>(value_cache),
                    block_stride * es, token_stride * es, head_stride * es, block_table,
                    table_stride, table_width, seq_lens, row_offsets, B, n_rows, max_len, heads,
-                   heads / kv_heads, head_dim, num_blocks, page_size, window, scale * kLog2e,
+                   heads / kv_heads, head_dim, num_blocks, page_size, window,
+                   c == 0.0f ? 1e-37f : c,  // masked scores stay -inf
                    static_cast<char*>(out), o_row_stride * es, o_head_stride * es, out_lse,
                    dev_error};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (on_tensor_cores(dtype, head_dim)) return run_mma(a, kv_heads, workspace, st);
   const int64_t items = static_cast<int64_t>(n_rows) * heads;
   const dim3 grid(static_cast<unsigned>((items + kRowWarps - 1) / kRowWarps));
   return es == 2 ? launch(attn_rows_kernel<__nv_bfloat16>, grid, kRowWarps * 32, 0, 1, false, st, a)

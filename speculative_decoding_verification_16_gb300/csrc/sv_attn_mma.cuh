@@ -1,0 +1,778 @@
+// sv_attn_mma.cuh -- the tensor core attention kernel (bf16, head_dim <= 128).
+//
+// The query rows of a request that share a key/value head -- l tokens times the
+// group of G heads -- are packed into tiles of 128 rows, row i = token i / G,
+// head i % G of the group, so a key/value tile is read once for all of them.
+// An item is (request, kv head, NS row tiles); its work is the 128-key tiles
+// from the first key that its first row sees to the last that its last row
+// sees.  All items' tiles in a row are cut into equal runs, one a worker (CTA);
+// a worker whose run starts or ends inside an item leaves an unnormalised
+// partial (O, m, l) in the workspace, and the combine kernel joins them.
+//
+// Per stream of 128 rows (one softmax warpgroup, a thread a row) and key tile:
+//   S = Q K^T   tcgen05.mma from shared memory into 128 tensor memory columns
+//   P = 2^(S c - m c), c = scale log2 e, rounded to bf16 over S's own columns
+//   O += P V    tcgen05.mma with P from tensor memory
+// The running maximum m of a row rises lazily: P may grow to 2^8 before O is
+// rescaled, so most tiles leave O alone; the row sum l is of the unrounded P, in
+// fp32.  P keeps 8 bits of mantissa: an error of at most 2^-9 a weight, of the
+// size of the output's own rounding, for tensor products at full rate.
+//
+// NS = 1 (at most 128 rows an item, decoding and verify steps: the cache's
+// bytes bound it): two CTAs an SM, each with one stream and a ring of 64-key
+// copies; while one's softmax runs, the other's products do.
+// NS = 2 (longer chunks: the products bound it): one CTA an SM, two streams
+// over the same key/value tiles, the tensor core alternating between them.
+//
+// Keys and values come by tensor copies of whole page pieces (page sizes that
+// are a multiple of 64 or 8, 16, 32) and by 16-byte copies of single rows
+// otherwise.
+//
+// Masked places.  S of a masked key is replaced, whatever it holds.  A masked
+// value is multiplied by P = 0, so a NaN or infinity there would reach every
+// row: in the tiles that not all rows see whole, V's non-finite elements under
+// keys that some row does not see are set to 0 in shared memory, and the
+// epilogue adds them, from the cache, to the rows that do see them.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "sv_ptx.cuh"
+#include "sv_tcgen05.cuh"
+
+namespace sv {
+namespace serve {
+
+constexpr int kTile = 128;        // keys of a tile
+constexpr int kMaxWorkers = 320;  // partials are laid out for this many
+constexpr float kRescale = 8.0f;  // log2 of how far P may exceed 1 before O is rescaled
+
+struct AttnRecord {  // where a worker's run starts inside an item (off > 0)
+  int32_t r, h, m, off, n;  // item, tiles of it before the run, its tiles
+  int32_t workers;
+  int64_t total;  // all tiles
+};
+
+struct MmaArgs {
+  AttnArgs a;
+  int32_t kv_heads, box;  // box: tokens of a tensor copy; 0: copies of single rows
+  AttnRecord* record;     // [kMaxWorkers]
+  float2* ml;             // [2 * kMaxWorkers][rows]: m c and l of the partials
+  float4* o;              // [2 * kMaxWorkers][DP / 4][rows]
+};
+
+__host__ __device__ constexpr int attn_unit_tokens(int ns) { return ns == 1 ? 64 : 128; }
+__host__ __device__ constexpr int attn_units(int ns, int dp) { return dp == 128 ? 5 : ns == 1 ? 10 : 10; }
+__host__ __device__ constexpr int attn_smem(int ns, int dp) {
+  return ns * kTile * dp * 2 + attn_units(ns, dp) * attn_unit_tokens(ns) * dp * 2 + 256;
+}
+
+// ---------------------------------------------------------------- work
+struct Segment {  // consecutive tiles of one item
+  int r, h, m;
+  int row0, l, seq;
+  int tile0, tile1;   // key tiles [tile0, tile1)
+  int rows;           // valid rows of the item
+  int kv_end;         // keys past the last one that any row sees
+  bool begins, whole;
+};
+
+struct ItemTiles {
+  int lo, n, rows, kv_end;
+};
+
+template <int MR>
+__device__ __forceinline__ ItemTiles item_tiles(const AttnArgs& a, const Span& s, int m) {
+  ItemTiles t;
+  const int all = s.l * a.group;
+  t.rows = min(MR, all - m * MR);
+  const int j0 = m * MR / a.group, j1 = (m * MR + t.rows - 1) / a.group;
+  t.kv_end = max(0, s.seq - s.l + j1 + 1);
+  const int kv_lo = a.window > 0 ? max(0, s.seq - s.l + j0 - a.window + 1) : 0;
+  t.lo = kv_lo / kTile;
+  t.n = max(1, (t.kv_end + kTile - 1) / kTile - t.lo);
+  return t;
+}
+
+template <int MR>
+__device__ __forceinline__ int64_t head_tiles(const AttnArgs& a, const Span& s) {
+  int64_t n = 0;
+  if (s.l > 0)
+    for (int m = 0; m * MR < s.l * a.group; ++m) n += item_tiles<MR>(a, s, m).n;
+  return n;
+}
+
+__device__ __forceinline__ int64_t worker_start(int64_t total, int workers, int w) {
+  return total * w / workers;
+}
+__device__ __forceinline__ int worker_of(int64_t total, int workers, int64_t u) {
+  return static_cast<int>(((u + 1) * workers - 1) / total);
+}
+
+template <int MR>
+struct Walk {  // a worker's segments in order
+  int r, h, m, off;
+  int64_t left;
+  Span s;
+
+  __device__ __forceinline__ bool next(const MmaArgs& p, Segment* g) {
+    if (left <= 0) return false;
+    const ItemTiles t = item_tiles<MR>(p.a, s, m);
+    const int take = static_cast<int>(min(left, static_cast<int64_t>(t.n - off)));
+    g->r = r, g->h = h, g->m = m, g->row0 = s.row0, g->l = s.l, g->seq = s.seq;
+    g->tile0 = t.lo + off, g->tile1 = t.lo + off + take;
+    g->rows = t.rows, g->kv_end = t.kv_end;
+    g->begins = off == 0, g->whole = off == 0 && take == t.n;
+    left -= take;
+    off += take;
+    if (off == t.n) {
+      off = 0;
+      if (++m * MR >= s.l * p.a.group) {
+        m = 0;
+        if (++h == p.kv_heads) {
+          h = 0;
+          if (left > 0) do s = span_of(p.a, ++r); while (s.l <= 0);
+        }
+      }
+    }
+    return true;
+  }
+};
+
+struct PlanSmem {
+  int64_t part[16];
+  int64_t total;
+  int64_t rem;
+  int r;
+};
+
+// Every CTA finds its own run: the requests' tiles are summed twice, once for
+// the total and once up to the run's start.
+template <int MR, int THREADS>
+__device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem* sm, Walk<MR>* w) {
+  const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kW = THREADS / 32;
+  int64_t mine = 0;
+  bool bad = false;
+  for (int r = tid; r < a.B; r += THREADS) {
+    const Span s = span_of(a, r);
+    bad |= s.l < 0;
+    mine += head_tiles<MR>(a, s);
+  }
+  if (bad && blockIdx.x == 0 && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_LEN);
+  int64_t sum = mine;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  if (lane == 0) sm->part[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+  for (int i = 0; i < kW; ++i) total += sm->part[i];
+  total *= p.kv_heads;
+  const int workers = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  const int me = blockIdx.x;
+  AttnRecord rec{0, 0, 0, 0, 0, workers, total};
+  bool any = me < workers;
+  if (any) {
+    const int64_t start = worker_start(total, workers, me);
+    __syncthreads();
+    int64_t carry = 0;
+    for (int base = 0; base < a.B; base += THREADS) {
+      const int r = base + tid;
+      const int64_t own =
+          (a.B <= THREADS ? mine : r < a.B ? head_tiles<MR>(a, span_of(a, r)) : 0) * p.kv_heads;
+      int64_t inc = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(~0u, inc, d);
+        if (lane >= d) inc += o;
+      }
+      if (lane == 31) sm->part[warp] = inc;
+      __syncthreads();
+      int64_t before = carry;
+      for (int i = 0; i < kW; ++i) {
+        if (i < warp) before += sm->part[i];
+        carry += sm->part[i];
+      }
+      if (before + inc - own <= start && start < before + inc)
+        sm->r = r, sm->rem = start - (before + inc - own);
+      __syncthreads();
+      if (carry > start) break;
+    }
+    w->r = sm->r;
+    w->s = span_of(a, w->r);
+    int64_t rem = sm->rem;
+    const int64_t per_head = head_tiles<MR>(a, w->s);
+    w->h = static_cast<int>(rem / per_head);
+    rem -= w->h * per_head;
+    w->m = 0;
+    int n = item_tiles<MR>(a, w->s, 0).n;
+    while (rem >= n) rem -= n, n = item_tiles<MR>(a, w->s, ++w->m).n;
+    w->off = static_cast<int>(rem);
+    w->left = worker_start(total, workers, me + 1) - start;
+    rec.r = w->r, rec.h = w->h, rec.m = w->m, rec.off = w->off, rec.n = n;
+  }
+  if (tid == 0) p.record[me] = rec;
+  return any;
+}
+
+// ---------------------------------------------------------------- kernel
+template <int NS, int DP>
+struct AttnSmem {
+  static constexpr int kUnitTokens = attn_unit_tokens(NS);
+  static constexpr int kUnits = attn_units(NS, DP);
+  static constexpr int kUnitBytes = kUnitTokens * DP * 2;
+  static constexpr int kQBytes = kTile * DP * 2;
+  static constexpr int kChunks = DP / 64;
+  static constexpr int kPerTile = kTile / kUnitTokens;  // units of a K or V tile
+};
+
+struct AttnBars {
+  uint64_t full[10], empty[10];
+  uint64_t q[2], s[2], p[2], o[2], idle;
+  uint32_t tmem;
+  int32_t odd;  // a non-finite value was set aside in this CTA
+};
+static_assert(sizeof(AttnBars) <= 256, "barrier block");
+
+template <int NS, int DP, bool TMA>
+__global__ __launch_bounds__((NS * 4 + 2) * 32, 3 - NS) void attn_mma_kernel(
+    const MmaArgs p, const __grid_constant__ CUtensorMap kmap,
+    const __grid_constant__ CUtensorMap vmap) {
+  using L = AttnSmem<NS, DP>;
+  constexpr int MR = NS * kTile;
+  constexpr int kThreads = (NS * 4 + 2) * 32;
+  constexpr uint32_t kCols = NS == 1 ? 256 : 512;
+  // tensor memory columns: S (and P) of each stream, then O of each
+  constexpr uint32_t kO = NS * kTile;
+  extern __shared__ __align__(1024) char smem[];
+  const AttnArgs& a = p.a;
+  char* const qbuf = smem;
+  char* const ring = smem + NS * L::kQBytes;
+  AttnBars* const bars = reinterpret_cast<AttnBars*>(ring + L::kUnits * L::kUnitBytes);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kLoadWarp = NS * 4, kMmaWarp = NS * 4 + 1;
+  bool timed_out = false;
+
+  Walk<MR> walk;
+  const bool any = plan<MR, kThreads>(p, reinterpret_cast<PlanSmem*>(ring), &walk);
+  grid_dep_launch_dependents();
+  if (!any) return;
+  __syncthreads();  // the plan's scratch becomes the ring
+  if (tid == 0) {
+    for (int i = 0; i < L::kUnits; ++i) {
+      mbar_init(smem_addr(&bars->full[i]), TMA ? 1 : 32);
+      mbar_init(smem_addr(&bars->empty[i]), 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_addr(&bars->q[s]), 128);
+      mbar_init(smem_addr(&bars->s[s]), 1);
+      mbar_init(smem_addr(&bars->p[s]), 128);
+      mbar_init(smem_addr(&bars->o[s]), 1);
+    }
+    mbar_init(smem_addr(&bars->idle), 1);
+    bars->odd = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_addr(&bars->tmem), kCols);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = bars->tmem;
+  const uint32_t ring_addr = smem_addr(ring), q_addr = smem_addr(qbuf);
+  auto full = [&](int u) { return smem_addr(&bars->full[u]); };
+  auto empty = [&](int u) { return smem_addr(&bars->empty[u]); };
+
+  if (warp == kLoadWarp) {
+    // ---------------------------------------------------------- copies
+    int u = 0;          // ring position
+    uint32_t turn = 0;  // parity of the ring's turn
+    int issued = 0;     // units issued so far
+    uint32_t err = 0;
+    Segment g;
+    while (walk.next(p, &g)) {
+      const int32_t* table = a.table + g.r * a.table_stride;
+      for (int tile = g.tile0; tile < g.tile1; ++tile) {
+        for (int half = 0; half < 2 * L::kPerTile; ++half) {
+          const bool val = half >= L::kPerTile;
+          const int t0 = tile * kTile + (half % L::kPerTile) * L::kUnitTokens;
+          const uint32_t dst = ring_addr + u * L::kUnitBytes;
+          if constexpr (TMA) {
+            // lane: box lane / chunks of the unit, column chunk lane % chunks
+            const int boxes = L::kUnitTokens / p.box;
+            const int t = t0 + lane / L::kChunks * p.box, c = lane % L::kChunks;
+            const bool on = lane < boxes * L::kChunks && t < g.kv_end;
+            int id = 0;
+            if (on) {
+              id = __ldg(table + t / a.page);
+              if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
+            }
+            const unsigned live = __ballot_sync(~0u, on);
+            if (issued >= L::kUnits) mbar_wait(empty(u), turn ^ 1, timed_out);
+            if (lane == 0)
+              mbar_arrive_expect_tx(full(u), static_cast<uint32_t>(__popc(live)) * p.box * 128);
+            __syncwarp();
+            if (on)
+              tma_load4(dst + c * (L::kUnitTokens * 128) + (t - t0) * 128, val ? &vmap : &kmap,
+                        c * 64, t % a.page, g.h, id, full(u));
+          } else {
+            // lane: the addresses of rows lane, lane + 32, ..; 16-byte pieces
+            constexpr int kRows = L::kUnitTokens / 32, kPieces = DP / 8;
+            const char* at[kRows];
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+              const int t = t0 + k * 32 + lane;
+              at[k] = nullptr;
+              if (t < g.kv_end) {
+                int id = __ldg(table + t / a.page);
+                if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
+                at[k] = (val ? a.v : a.k) + id * a.block + (t % a.page) * a.token + g.h * a.head;
+              }
+            }
+            if (issued >= L::kUnits) mbar_wait(empty(u), turn ^ 1, timed_out);
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+              for (int i = 0; i < kPieces; ++i) {
+                const int row = i * 32 / kPieces + lane / kPieces, j = lane % kPieces;
+                const char* src = reinterpret_cast<const char*>(
+                    __shfl_sync(~0u, reinterpret_cast<unsigned long long>(at[k]), row));
+                const int rr = k * 32 + row;
+                const bool on = src != nullptr && j * 8 < a.dim;
+                cp_async16(dst + (j / 8) * (L::kUnitTokens * 128) + rr * 128 +
+                               (((j & 7) ^ (rr & 7)) << 4),
+                           on ? src + j * 16 : a.k, on ? 16 : 0);
+              }
+            cp_async_commit();
+            // the unit before the last has landed: hand it over
+            if (issued >= 2) {
+              cp_async_wait<2>();
+              fence_async_smem();
+              mbar_arrive(full((u + L::kUnits - 2) % L::kUnits));
+            }
+          }
+          ++issued;
+          if (++u == L::kUnits) u = 0, turn ^= 1;
+        }
+      }
+    }
+    if constexpr (!TMA) {
+      if (issued >= 2) {
+        cp_async_wait<1>();
+        fence_async_smem();
+        mbar_arrive(full((u + L::kUnits - 2) % L::kUnits));
+      }
+      cp_async_wait<0>();
+      fence_async_smem();
+      mbar_arrive(full((u + L::kUnits - 1) % L::kUnits));
+    } else if (timed_out) {  // no copy outlives the CTA (units issued late wait for their own)
+      for (int i = 0; i < L::kUnits; ++i) {
+        bool late = false;
+        mbar_wait(full(i), turn ^ (i < u ? 0u : 1u), late);
+      }
+    }
+    if (err != 0 && a.dev_error != nullptr) atomicOr(a.dev_error, static_cast<int32_t>(err));
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t kQk = mma_idesc(L::kUnitTokens, false), kPv = mma_idesc(DP, true);
+      int u = 0;
+      uint32_t turn = 0;          // parity of the ring's turn
+      uint32_t pturn[2] = {0, 0};  // parity of each stream's next P
+      uint32_t qturn = 0;
+      auto wait_unit = [&](int unit, uint32_t par) {
+        mbar_wait(full(unit), par, timed_out);
+        tmem_fence_after();
+      };
+      // S columns [n0, n0 + unit) of stream s from the unit at `kb`
+      auto qk = [&](int s, uint32_t kb, int n0) {
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t at = (k % 4) * 32;
+          mma_ss(tmem + s * kTile + n0,
+                 smem_desc(q_addr + s * L::kQBytes + k / 4 * (kTile * 128) + at, 0),
+                 smem_desc(kb + k / 4 * (L::kUnitTokens * 128) + at, 0), kQk, k > 0);
+        }
+      };
+      auto pv = [&](int s, uint32_t vb, int k0, bool add) {
+#pragma unroll
+        for (int k = 0; k < L::kUnitTokens / 16; ++k)
+          mma_ts(tmem + kO + s * DP, tmem + s * kTile + (k0 + k * 16) / 2,
+                 smem_desc(vb + k * 2048, DP > 64 ? L::kUnitTokens * 128 : 0), kPv, add || k > 0);
+      };
+      Segment g;
+      if constexpr (NS == 1) {
+        while (walk.next(p, &g)) {
+          mbar_wait(smem_addr(&bars->q[0]), qturn, timed_out);
+          qturn ^= 1;
+          for (int tile = g.tile0; tile < g.tile1; ++tile) {
+#pragma unroll
+            for (int i = 0; i < L::kPerTile; ++i) {
+              wait_unit(u, turn);
+              qk(0, ring_addr + u * L::kUnitBytes, i * L::kUnitTokens);
+              mma_commit(empty(u));
+              if (++u == L::kUnits) u = 0, turn ^= 1;
+            }
+            mma_commit(smem_addr(&bars->s[0]));
+            mbar_wait(smem_addr(&bars->p[0]), pturn[0], timed_out);
+            pturn[0] ^= 1;
+            tmem_fence_after();
+#pragma unroll
+            for (int i = 0; i < L::kPerTile; ++i) {
+              wait_unit(u, turn);
+              pv(0, ring_addr + u * L::kUnitBytes, i * L::kUnitTokens, tile > g.tile0 || i > 0);
+              mma_commit(empty(u));
+              if (++u == L::kUnits) u = 0, turn ^= 1;
+            }
+            mma_commit(smem_addr(&bars->o[0]));
+          }
+        }
+      } else {
+        auto step = [&]() {
+          if (++u == L::kUnits) u = 0, turn ^= 1;
+        };
+        while (walk.next(p, &g)) {
+          const int ns = g.rows > kTile ? 2 : 1;
+          for (int s = 0; s < 2; ++s) mbar_wait(smem_addr(&bars->q[s]), qturn, timed_out);
+          qturn ^= 1;
+          if (ns == 1) mbar_arrive(smem_addr(&bars->idle));  // the second stream may go on
+          wait_unit(u, turn);
+          for (int s = 0; s < ns; ++s) {
+            qk(s, ring_addr + u * L::kUnitBytes, 0);
+            if (s == ns - 1) mma_commit(empty(u));
+            mma_commit(smem_addr(&bars->s[s]));
+          }
+          step();
+          for (int tile = g.tile0; tile < g.tile1; ++tile) {
+            const int vu = u;
+            const uint32_t vt = turn;
+            step();
+            for (int s = 0; s < ns; ++s) {
+              mbar_wait(smem_addr(&bars->p[s]), pturn[s], timed_out);
+              pturn[s] ^= 1;
+              tmem_fence_after();
+              if (s == 0) wait_unit(vu, vt);
+              pv(s, ring_addr + vu * L::kUnitBytes, 0, tile > g.tile0);
+              if (s == ns - 1) mma_commit(empty(vu));
+              mma_commit(smem_addr(&bars->o[s]));
+              if (tile + 1 < g.tile1) {
+                if (s == 0) wait_unit(u, turn);
+                qk(s, ring_addr + u * L::kUnitBytes, 0);
+                if (s == ns - 1) mma_commit(empty(u));
+                mma_commit(smem_addr(&bars->s[s]));
+              }
+            }
+            if (tile + 1 < g.tile1) step();
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- softmax
+    const int st = warp >> 2;          // stream
+    const int row = tid & 127;         // row of the stream's tile
+    const int wrow = (warp & 3) * 32;  // the warp's first row
+    const uint32_t lanes = static_cast<uint32_t>(wrow) << 16;
+    const uint32_t s_at = tmem + lanes + st * kTile, o_at = tmem + lanes + kO + st * DP;
+    const uint32_t qdst = q_addr + st * L::kQBytes;
+    const uint32_t qbar = smem_addr(&bars->q[st]), sbar = smem_addr(&bars->s[st]),
+                   pbar = smem_addr(&bars->p[st]), obar = smem_addr(&bars->o[st]);
+    const bool neg = a.scale2 < 0.0f;
+    const float c = fabsf(a.scale2);
+    uint32_t turn = 0;  // parity of the stream's next tile
+    uint32_t idle = 0;  // parity of the next segment without rows here
+    int vu = 0;         // ring position of the tile's first V unit
+    uint32_t vturn = 0;
+    auto ring_step = [&](int n) {
+      vu += n;
+      if (vu >= L::kUnits) vu -= L::kUnits, vturn ^= 1;
+    };
+
+    // the query rows of a segment: lane's own row address, then 16-byte pieces
+    auto load_q = [&](const Segment& g) {
+      const int i = g.m * MR + st * kTile + wrow + lane;
+      const bool on = st * kTile + wrow + lane < g.rows;
+      const char* src = nullptr;
+      if (on)
+        src = a.q + static_cast<int64_t>(g.row0 + i / a.group) * a.q_row +
+              static_cast<int64_t>(g.h * a.group + i % a.group) * a.q_head;
+      constexpr int kPieces = DP / 8;
+      if (st * kTile + wrow < g.rows) {
+#pragma unroll 4
+        for (int k = 0; k < kPieces; ++k) {
+          const int rr = k * 32 / kPieces + lane / kPieces, j = lane % kPieces;
+          const char* from = reinterpret_cast<const char*>(
+              __shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), rr));
+          const bool ok = from != nullptr && j * 8 < a.dim;
+          cp_async16(qdst + (j / 8) * (kTile * 128) + (wrow + rr) * 128 + (((j & 7) ^ (rr & 7)) << 4),
+                     ok ? from + j * 16 : a.q, ok ? 16 : 0);
+        }
+      }
+      cp_async_commit();
+    };
+
+    Segment g, next;
+    bool more = walk.next(p, &g);
+    load_q(g);
+    while (more) {
+      cp_async_wait<0>();
+      fence_async_smem();
+      mbar_arrive(qbar);
+      const bool has_next = walk.next(p, &next);
+      const bool live = st * kTile < g.rows;          // the stream has rows
+      const bool work = st * kTile + wrow < g.rows;   // the warp has rows
+      const int token = (g.m * MR + st * kTile + row) / a.group;  // of this thread's row
+      const int pos = g.seq - g.l + token;
+      const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      // keys that every row of the item sees: [all_lo, all_hi)
+      const int all_hi = g.seq - g.l + g.m * MR / a.group + 1;
+      const int all_lo = a.window > 0
+          ? max(0, g.seq - g.l + (g.m * MR + g.rows - 1) / a.group - a.window + 1) : 0;
+      float m = -kInf, l = 0.0f;
+
+      if (!live) {  // the other stream's tiles pass through the ring
+        mbar_wait(smem_addr(&bars->idle), idle, timed_out);
+        idle ^= 1;
+        for (int tile = g.tile0; tile < g.tile1; ++tile) ring_step(2 * L::kPerTile);
+        if (has_next) load_q(next);
+      }
+      for (int tile = g.tile0; live && tile < g.tile1; ++tile) {
+        const int t0 = tile * kTile;
+        ring_step(L::kPerTile);  // past K: at V
+        const bool edge = t0 + kTile > all_hi || t0 < all_lo;
+        if (edge) {  // set aside non-finite values that not all rows see
+          int un = vu;
+          uint32_t ut = vturn;
+#pragma unroll
+          for (int i = 0; i < L::kPerTile; ++i) {
+            mbar_wait(full(un), ut, timed_out);
+            char* unit = ring + un * L::kUnitBytes;
+            for (int at = row; at < L::kUnitBytes / 16; at += 128) {
+              const int t = t0 + i * L::kUnitTokens + (at >> 3) % L::kUnitTokens;
+              if (t >= all_lo && t < all_hi) continue;
+              uint4 v = *reinterpret_cast<const uint4*>(unit + at * 16);
+              uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, odd = true;
+                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, odd = true;
+              }
+              if (odd) {
+                if (t < g.seq) bars->odd = 1;
+                __threadfence_block();
+                *reinterpret_cast<uint4*>(unit + at * 16) = v;
+              }
+            }
+            if (++un == L::kUnits) un = 0, ut ^= 1;
+          }
+          fence_async_smem();
+        }
+        mbar_wait(sbar, turn, timed_out);
+        __syncwarp();
+        tmem_fence_after();
+        if (tile + 1 == g.tile1 && has_next) load_q(next);  // the last S is formed: Q is free
+        if (work) {
+          uint32_t x[kTile];
+#pragma unroll
+          for (int k = 0; k < kTile; k += 32) tmem_ld32(s_at + k, x + k);
+          tmem_wait_ld();
+          float* s = reinterpret_cast<float*>(x);
+          if (neg) {
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) s[k] = -s[k];
+          }
+          if (edge) {
+            const int from = lo - t0, to = pos + 1 - t0;
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) s[k] = k >= from && k < to ? s[k] : -kInf;
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int k = 4; k < kTile; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
+          const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (tile == g.tile0) {
+            m = top;
+          } else {
+            const bool rise = top > -kInf && (m == -kInf || (top - m) * c > kRescale);
+            if (__any_sync(~0u, rise)) {
+              const float f = top > m ? ex2((m - top) * c) : 1.0f;
+              mbar_wait(obar, turn ^ 1, timed_out);
+              __syncwarp();
+              tmem_fence_after();
+#pragma unroll
+              for (int k = 0; k < DP; k += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_at + k, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(o_at + k, o);
+              }
+              l *= f;
+              m = top;
+            }
+          }
+          float base = m == -kInf ? 0.0f : m * c, mul = c;
+          if (__any_sync(~0u, fabsf(base) > 0x1p20f)) {
+            // scores so large that the rounding of m c would not cancel in s c - m c
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) s[k] = (s[k] - (m == -kInf ? 0.0f : m)) * c;
+            base = 0.0f, mul = 1.0f;
+          }
+          float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < kTile; k += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = ex2(fmaf(s[k + 2 * e], mul, -base));
+              const float p1 = ex2(fmaf(s[k + 2 * e + 1], mul, -base));
+              sum[e & 1] += p0, sum[2 + (e & 1)] += p1;
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(p1), "f"(p0));
+            }
+            tmem_st16(s_at + k / 2, w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        tmem_fence_before();
+        mbar_arrive(pbar);
+        turn ^= 1;
+        ring_step(L::kPerTile);
+      }
+
+      if (live) {
+        // ------------------------------------------------------ epilogue
+        mbar_wait(obar, turn ^ 1, timed_out);
+        __syncwarp();
+        tmem_fence_after();
+        if (work) {
+          const bool valid = st * kTile + row < g.rows;
+          const bool odd = *reinterpret_cast<volatile int32_t*>(&bars->odd) != 0;
+          const int head = g.h * a.group + (g.m * MR + st * kTile + row) % a.group;
+          const int64_t orow = g.row0 + token;
+          const int slot = 2 * blockIdx.x + (g.begins ? 1 : 0);
+          const float inv = g.whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+          const int prow = st * kTile + row;
+#pragma unroll 1
+          for (int k = 0; k < DP; k += 32) {
+            uint32_t x[32];
+            tmem_ld32(o_at + k, x);
+            tmem_wait_ld();
+            float* o = reinterpret_cast<float*>(x);
+            __syncwarp();
+            if (!valid) continue;
+            if (odd) {  // values set aside that this row sees
+              for (int t = max(g.tile0 * kTile, lo); t < min(g.tile1 * kTile, pos + 1); ++t) {
+                if (t >= all_lo && t < all_hi) {
+                  t = min(all_hi, pos + 1) - 1;
+                  continue;
+                }
+                int id = a.table[g.r * a.table_stride + t / a.page];
+                if (id < 0 || id >= a.num_blocks) id = 0;
+                const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
+                    a.v + id * a.block + (t % a.page) * a.token + g.h * a.head) + k;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (k + e < a.dim && !(fabsf(__bfloat162float(v[e])) < kInf))
+                    o[e] += __bfloat162float(v[e]);
+              }
+            }
+            if (g.whole) {
+              char* out = a.out + orow * a.o_row + head * a.o_head + k * 2;
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint4 w;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(o[e + 1] * inv), "f"(o[e] * inv));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(o[e + 3] * inv), "f"(o[e + 2] * inv));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.z) : "f"(o[e + 5] * inv), "f"(o[e + 4] * inv));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.w) : "f"(o[e + 7] * inv), "f"(o[e + 6] * inv));
+                if (k + e < a.dim) *reinterpret_cast<uint4*>(out + e * 2) = w;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                p.o[(static_cast<int64_t>(slot) * (DP / 4) + (k + e) / 4) * MR + prow] =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
+          if (valid) {
+            const float mc = m == -kInf ? -kInf : m * c;
+            if (!g.whole)
+              p.ml[static_cast<int64_t>(slot) * MR + prow] = make_float2(mc, l);
+            else if (a.lse != nullptr)
+              a.lse[orow * a.heads + head] = l > 0.0f || l != l ? (mc + log2f(l)) * kLn2 : -kInf;
+          }
+          tmem_fence_before();
+        }
+      }
+      g = next;
+      more = has_next;
+    }
+  }
+  if (timed_out && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_TIMEOUT);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, kCols);
+}
+
+// ---------------------------------------------------------------- combine
+//
+// Joins the partials of the items that were cut: the block of a worker whose
+// run starts inside an item, if it is the first such worker, sums the item's
+// parts in worker order.  A thread a row, four columns at a time.
+constexpr int kCombineThreads = 128;
+constexpr int kCombineRows = 16;
+
+template <int MR, int DP>
+__global__ __launch_bounds__(kCombineThreads) void attn_combine_kernel(const MmaArgs p) {
+  grid_dep_wait();
+  const AttnArgs& a = p.a;
+  const int w = blockIdx.x;
+  const AttnRecord rec = p.record[w];
+  if (rec.off == 0) return;
+  const int64_t u0 = worker_start(rec.total, rec.workers, w) - rec.off;
+  const int w0 = worker_of(rec.total, rec.workers, u0);
+  if (w0 != w - 1) return;
+  const int w1 = worker_of(rec.total, rec.workers, u0 + rec.n - 1);
+  const Span s = span_of(a, rec.r);
+  const int rows = min(MR, s.l * a.group - rec.m * MR);
+  const int row = blockIdx.y * kCombineRows + (threadIdx.x % kCombineRows);
+  if (row >= rows) return;
+  float top = -kInf;
+  for (int i = w0; i <= w1; ++i)
+    top = fmaxf(top, p.ml[static_cast<int64_t>(2 * i + (i == w0 ? 1 : 0)) * MR + row].x);
+  const float base = top == -kInf ? 0.0f : top;
+  float l = 0;
+  for (int i = w0; i <= w1; ++i) {
+    const float2 x = p.ml[static_cast<int64_t>(2 * i + (i == w0 ? 1 : 0)) * MR + row];
+    l += x.y * ex2(x.x - base);
+  }
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  const int i = rec.m * MR + row;
+  const int64_t orow = s.row0 + i / a.group;
+  const int head = rec.h * a.group + i % a.group;
+  for (int q = threadIdx.x / kCombineRows; q < DP / 4; q += kCombineThreads / kCombineRows) {
+    if (q * 4 >= a.dim) break;
+    float4 o = make_float4(0, 0, 0, 0);
+    for (int j = w0; j <= w1; ++j) {
+      const int slot = 2 * j + (j == w0 ? 1 : 0);
+      const float f = ex2(p.ml[static_cast<int64_t>(slot) * MR + row].x - base);
+      const float4 x = p.o[(static_cast<int64_t>(slot) * (DP / 4) + q) * MR + row];
+      o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y);
+      o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
+    }
+    uint2 v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(o.y * inv), "f"(o.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(o.w * inv), "f"(o.z * inv));
+    *reinterpret_cast<uint2*>(a.out + orow * a.o_row + head * a.o_head + q * 8) = v;
+  }
+  if (threadIdx.x < kCombineRows && a.lse != nullptr)
+    a.lse[orow * a.heads + head] = l > 0.0f || l != l ? (base + log2f(l)) * kLn2 : -kInf;
+}
+
+}  // namespace serve
+}  // namespace sv
