@@ -1,25 +1,27 @@
 // sv_sample.cu -- one token per row with per-row temperature, top-k, top-p and
 // min-p from given random numbers (include/spec_verify_serve.h).
 //
-// A cluster of C CTAs owns a row: each copies its slice of the row to shared
-// memory once (cp.async.bulk, one copy and one barrier a warp), and every pass
-// reads it there, so a logit crosses HBM once whatever the filters need.  A
-// pass ends with an exchange: each CTA stores its partial into every CTA's
-// shared memory, and after the cluster barrier all sum the C partials in rank
-// order, so all decide alike.
-//
-// The kept set is a prefix of the order (value desc, id asc), so its last
-// token (value t, id) describes it; min-p is a bar on the weight itself.
-//  - Max pass: the row's maximum, and from every warp the largest of its lanes'
-//    maxima, 256 seeds a row: R elements are at or above the R-th largest seed.
-//  - Collect pass: the tokens at or above that bar go to a list (R = top_k, or
-//    192 for top-p alone, whose pass also sums the row's mass).  If the list
-//    holds the top-k set, or top_p of the mass, rank 0 finishes on it: ranks by
+// A cluster of C CTAs owns a row and streams it from HBM once.  It keeps, for
+// every group of G 16-byte vectors (at most 512 bytes), the largest logit and,
+// where the row's mass is needed, the group's mass relative to it, both in
+// shared memory of rank 0, which then decides alone.  The kept set is a prefix of
+// the order (value desc, id asc), so its last token (value t, id) describes it;
+// min-p is a bar on the weight itself.
+//  - No filter: the masses pick the group, one group is read again (from L2).
+//  - Filters: at least R tokens are at or above the R-th largest group maximum.
+//    With R = top_k, or 192 for top-p alone, only the groups that reach this bar
+//    are read again, and their tokens at or above it make a list.  If it holds
+//    the top-k set, or top_p of the mass, the row is finished on it: ranks by
 //    counting, the cuts, the draw.  This is the path of usual rows.
-//  - Otherwise a search narrows an interval of values around the cut, three
-//    pivots a pass, placed by interpolation, until the interval holds at most
-//    kList tokens, which are collected and ranked, or one value (ties).
-//    Then one pass draws over the slices.
+//  - Otherwise (flat rows under top-p, top_k of hundreds, many ties) all CTAs of
+//    the row search: an interval of values around the cut is narrowed, three
+//    pivots a pass over the row (from L2), placed by interpolation, until it
+//    holds at most kList tokens, which are collected and ranked, or one value.
+//    Then one pass forms the groups' kept masses, and the draw is as without
+//    filters.
+// A pass of the search ends with an exchange: each CTA stores its partial into
+// every CTA's shared memory, and after the cluster barrier all sum the C
+// partials in rank order, so all decide alike.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,12 +37,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kList = 512;      // most tokens of a list
+constexpr int kTopPSeeds = 192;  // group maxima that a top-p row's bar lies below
 constexpr float kInf = __builtin_huge_valf();
 
 struct SampleArgs {
   const char* logits;
   int64_t row_bytes;
-  int32_t V, C, L;  // CTAs a row, elements a slice
+  int32_t V, C, slice, G, stats;  // CTAs a row, vectors a slice, vectors a group, most groups
   const float* temperature;
   const int32_t* top_k;
   const float *top_p, *min_p, *uniforms;
@@ -49,21 +53,16 @@ struct SampleArgs {
   int32_t* dev_error;
 };
 
-constexpr int kSeeds = 256;  // of a row, over all its warps
-constexpr int kList = 512;   // most tokens of a list
-constexpr int kTopPSeeds = 192;
-
 struct Header {
   float4 slot[2][kMaxCluster][2];  // exchanged partials, two exchanges in turn
   float4 part[kWarps][2];
-  uint64_t bar[kWarps];
-  uint64_t all[kList];   // rank 0: every CTA's list; key above complemented id
-  uint64_t list[kList];  // this CTA's
-  float w[kList];        // rank 0: weights and ids, best first
+  uint64_t all[kList];  // rank 0: the list; key above complemented id
+  float w[kList];       // rank 0: weights and ids, best first
   int32_t id[kList];
-  uint16_t seed[kSeeds];
-  int32_t count, pick, cut;
-  float kept, total;
+  int32_t bits[2][kWarps];
+  int32_t count, pick, cut, group, groups;
+  float kept, total, base;
+  int32_t verdict;  // 0: done, 1: search
 };
 constexpr int kHeaderBytes = (sizeof(Header) + 127) / 128 * 128;
 
@@ -134,16 +133,62 @@ __device__ __forceinline__ float value_of(uint64_t e) {
 }
 __device__ __forceinline__ int id_of(uint64_t e) { return static_cast<int>(~static_cast<uint32_t>(e)); }
 
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
+  uint32_t peer;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(smem_addr(p)), "r"(rank));
+  return peer;
+}
+
 template <int ES>
 struct Row {
   static constexpr int N = 16 / ES;
   Header* h;
-  const uint4* data;    // this CTA's slice, 16-byte vectors
-  int v_first, v_last;  // this warp's run of them
-  int first;            // token id of vector 0's element 0 (may start before the slice)
-  int begin, end;       // token ids of the slice
-  int C, rank, parity = 0;
-  float best, sc;       // the row's maximum, log2(e) / T
+  float2* stat;          // rank 0: (largest logit, mass) of every group
+  const char* base;      // the row, from the 16-byte boundary at or below it
+  int lead, nvec;        // elements before the row in vector 0; its vectors
+  int v0, v1;            // this CTA's vectors
+  int V, G, C, rank, parity = 0;
+  float best, sc;        // the row's maximum, log2(e) / T
+
+  // Vector i; what the first and last hold beside the row is -inf.
+  __device__ __forceinline__ uint4 load(int i) const {
+    const char* p = base + static_cast<int64_t>(i) * 16;
+    if (i * N >= lead && (i + 1) * N <= lead + V) return __ldg(reinterpret_cast<const uint4*>(p));
+    union {
+      uint4 v;
+      uint16_t s[8];
+      float f[4];
+    } x;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int id = i * N + e - lead;
+      const bool in = id >= 0 && id < V;
+      if constexpr (ES == 2) x.s[e] = in ? reinterpret_cast<const uint16_t*>(p)[e] : 0xff80u;
+      else x.f[e] = in ? reinterpret_cast<const float*>(p)[e] : -kInf;
+    }
+    return x.v;
+  }
+
+  // f(vector index, vector, valid) over this CTA's vectors: a warp 32 together,
+  // four loads in flight; every lane takes part in every call.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i0 = v0 + warp * 32; i0 < v1; i0 += kThreads * 4) {
+      uint4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kThreads + lane;
+        const uint32_t pad = ES == 2 ? 0xff80ff80u : 0xff800000u;
+        x[k] = i < v1 ? load(i) : make_uint4(pad, pad, pad, pad);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k * kThreads < v1) f(i0 + k * kThreads + lane, x[k]);
+    }
+  }
+
+  __device__ __forceinline__ int token(int vec, int e) const { return vec * N + e - lead; }
 
   // Every CTA's partial, in rank order, to every thread.
   __device__ __forceinline__ const float4 (*exchange(float4 a, float4 b))[2] {
@@ -158,8 +203,8 @@ struct Row {
     return s;
   }
 
-  // The warps' partials (floats a.xyz, integers b.xyz) summed over the CTA in
-  // warp order, then over the row in rank order.
+  // The threads' partials summed over warps, the CTA in warp order, and the row
+  // in rank order.
   struct Sums {
     float m[3];
     int c[3];
@@ -199,8 +244,8 @@ struct Row {
   __device__ __forceinline__ Sums at_least(const float t[3]) {
     Sums v{{0, 0, 0}, {0, 0, 0}};
     const float low = fminf(t[0], fminf(t[1], t[2]));
-    for (int i = v_first + (threadIdx.x & 31); i < v_last; i += 32) {
-      const Vec<ES> x(data[i]);
+    each([&](int, const uint4& raw) {
+      const Vec<ES> x(raw);
 #pragma unroll
       for (int e = 0; e < N; ++e)
         if (x.x[e] >= low) {
@@ -209,26 +254,22 @@ struct Row {
           for (int j = 0; j < 3; ++j)
             if (x.x[e] >= t[j]) v.m[j] += w, ++v.c[j];
         }
-    }
+    });
     return total(v);
   }
 
+  // Into rank 0's list, from any CTA of the row.
   __device__ __forceinline__ void append(float x, int id) {
-    if (id < begin || id >= end) return;  // what the edge vectors hold beside the slice
-    const int at = atomicAdd(&h->count, 1);
-    if (at < kList) h->list[at] = entry_of(x, id);
-  }
-
-  // This CTA's list (of h->count tokens) into rank 0's, behind those of the
-  // ranks before it (`before` tokens).
-  __device__ __forceinline__ void send(int before) {
-    const int n = h->count;
-    uint32_t peer;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(smem_addr(h->all)), "r"(0));
-    for (int i = threadIdx.x; i < n; i += kThreads)
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer + (before + i) * 8), "l"(h->list[i])
+    if (id < 0 || id >= V) return;
+    int at;
+    asm volatile("atom.relaxed.cluster.shared::cluster.add.s32 %0, [%1], 1;"
+                 : "=r"(at)
+                 : "r"(peer_addr(&h->count, 0))
+                 : "memory");
+    if (at < kList)
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_addr(h->all, 0) + at * 8),
+                   "l"(entry_of(x, id))
                    : "memory");
-    cluster_sync();
   }
 
   // Rank 0: weights and ids of the n listed tokens, best first.
@@ -243,7 +284,7 @@ struct Row {
     __syncthreads();
   }
 
-  // Warp 0 of rank 0, over the ranked list: the first index (from 1) whose
+  // A warp of rank 0, over the ranked list: the first index (from 1) whose
   // running sum of weights reaches `need`, n if none does; *sum gets the sum
   // up to there.
   __device__ __forceinline__ int reach(int n, float need, float* sum) {
@@ -329,25 +370,17 @@ __device__ __noinline__ Cut search(Row<ES>& R, int k, float need, uint32_t lo, i
   const bool top = hi > key_of<ES>(R.best);  // nothing lies above
   Cut cut;
   if (c_lo - c_hi <= kList) {  // the few tokens of the interval, ranked
-    __syncthreads();
     if (tid == 0) h->count = 0;
-    __syncthreads();
-    for (int i = R.v_first + lane; i < R.v_last; i += 32) {
-      const Vec<ES> v(R.data[i]);
+    cluster_sync();
+    R.each([&](int i, const uint4& raw) {
+      const Vec<ES> v(raw);
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (v.x[e] >= tl && (top || v.x[e] < th)) R.append(v.x[e], R.first + i * N + e);
-    }
-    __syncthreads();
-    const float4(*s)[2] = R.exchange(make_float4(__int_as_float(h->count), 0, 0, 0),
-                                     make_float4(0, 0, 0, 0));
-    int before = 0, n = 0;
-    for (int r = 0; r < R.C; ++r) {
-      if (r < R.rank) before += __float_as_int(s[r][0].x);
-      n += __float_as_int(s[r][0].x);
-    }
-    R.send(before);
+        if (v.x[e] >= tl && (top || v.x[e] < th)) R.append(v.x[e], R.token(i, e));
+    });
+    cluster_sync();
     if (R.rank == 0) {
+      const int n = min(h->count, kList);
       R.rank_list(n);
       if (warp == 0) {
         float sum;
@@ -379,9 +412,12 @@ __device__ __noinline__ Cut search(Row<ES>& R, int k, float need, uint32_t lo, i
       ties = k - c_hi;
     }
     cut.mass = m_hi + static_cast<float>(ties) * w;
+    // per warp's run of the CTA's vectors, so that ids ascend over runs and ranks
+    const int run = (R.v1 - R.v0 + kWarps - 1) / kWarps;
+    const int r0 = min(R.v1, R.v0 + warp * run), r1 = min(R.v1, r0 + run);
     int c = 0;
-    for (int i = R.v_first + lane; i < R.v_last; i += 32) {
-      const Vec<ES> v(R.data[i]);
+    for (int i = r0 + lane; i < r1; i += 32) {
+      const Vec<ES> v(R.load(i));
 #pragma unroll
       for (int e = 0; e < N; ++e) c += v.x[e] == cut.t ? 1 : 0;
     }
@@ -403,11 +439,11 @@ __device__ __noinline__ Cut search(Row<ES>& R, int k, float need, uint32_t lo, i
     }
     if (ties < all && before < ties && before + mine >= ties) {  // this warp's run holds it
       int left = static_cast<int>(ties) - before;
-      for (int i0 = R.v_first; i0 < R.v_last; i0 += 32) {
+      for (int i0 = r0; i0 < r1; i0 += 32) {
         const int i = i0 + lane;
         int n = 0;
-        if (i < R.v_last) {
-          const Vec<ES> v(R.data[i]);
+        if (i < r1) {
+          const Vec<ES> v(R.load(i));
 #pragma unroll
           for (int e = 0; e < N; ++e) n += v.x[e] == cut.t ? 1 : 0;
         }
@@ -417,12 +453,12 @@ __device__ __noinline__ Cut search(Row<ES>& R, int k, float need, uint32_t lo, i
           const int o = __shfl_up_sync(~0u, inc, d);
           if (lane >= d) inc += o;
         }
-        if (i < R.v_last && inc - n < left && inc >= left) {
-          const Vec<ES> v(R.data[i]);
+        if (i < r1 && inc - n < left && inc >= left) {
+          const Vec<ES> v(R.load(i));
           int seen = inc - n;
 #pragma unroll
           for (int e = 0; e < N; ++e)
-            if (v.x[e] == cut.t && ++seen == left) h->pick = R.first + i * N + e;
+            if (v.x[e] == cut.t && ++seen == left) h->pick = R.token(i, e);
         }
         const int step = __shfl_sync(~0u, inc, 31);
         if (step >= left) break;
@@ -441,56 +477,111 @@ __device__ __noinline__ Cut search(Row<ES>& R, int k, float need, uint32_t lo, i
   return cut;
 }
 
+// Rank 0: the token, from the groups' masses stat[].y (relative to the best
+// token): the group that holds u * total, then its tokens.
 template <int ES>
-__global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
+__device__ __forceinline__ void draw(Row<ES>& R, const SampleArgs& a, int row, int groups, float u,
+                                     Cut cut, float min_p) {
+  constexpr int N = 16 / ES;
+  Header* h = R.h;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (groups + kThreads - 1) / kThreads;
+  const int g0 = min(groups, tid * per), g1 = min(groups, g0 + per);
+  float own = 0;
+  for (int g = g0; g < g1; ++g) own += R.stat[g].y;
+  float inc = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const float o = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += o;
+  }
+  __syncthreads();
+  if (lane == 31) h->part[warp][0].x = inc;
+  if (tid == 0) h->pick = INT32_MAX, h->cut = -1;
+  __syncthreads();
+  float before = 0, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += h->part[w][0].x;
+    total += h->part[w][0].x;
+  }
+  const float target = u * total;
+  float cum = before + (inc - own);
+  if (own > 0.0f) {
+    if (cum + own > target) atomicMin(&h->pick, tid);
+    atomicMax(&h->cut, tid);
+  }
+  __syncthreads();
+  if (tid == (h->pick != INT32_MAX ? h->pick : h->cut)) {
+    int last = g0;
+    float base = cum;
+    for (int g = g0; g < g1; ++g) {
+      const float m = R.stat[g].y;
+      if (m > 0.0f) last = g, base = cum;
+      cum += m;
+      if (m > 0.0f && cum > target) break;
+    }
+    h->group = last, h->base = base;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  const int vec = h->group * R.G + lane;
+  float w[N], k = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) w[e] = 0;
+  if (lane < R.G && vec < R.nvec) {
+    const Vec<ES> v(R.load(vec));
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float x = v.x[e];
+      if (x > cut.t || (x == cut.t && R.token(vec, e) <= cut.id)) w[e] = R.weight(x);
+      if (w[e] < min_p) w[e] = 0.0f;
+      k += w[e];
+    }
+  }
+  inc = k;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const float o = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += o;
+  }
+  float c = h->base + (inc - k);
+  int id = -1, last = -1;
+  float iw = 0, lw = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    c += w[e];
+    if (w[e] > 0.0f) {
+      last = R.token(vec, e), lw = w[e];
+      if (id < 0 && c > target) id = last, iw = w[e];
+    }
+  }
+  const unsigned hit = __ballot_sync(~0u, id >= 0), any = __ballot_sync(~0u, last >= 0);
+  // without a hit the sums' rounding left the target past the group: its last token
+  const int from = hit != 0 ? __ffs(hit) - 1 : 31 - __clz(any);
+  if (lane == from) {
+    a.out_tokens[row] = hit != 0 ? id : last;
+    if (a.out_probs != nullptr) a.out_probs[row] = (hit != 0 ? iw : lw) / total;
+  }
+}
+
+template <int ES>
+__global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(128) char smem[];
   constexpr int N = 16 / ES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / a.C, rank = a.C > 1 ? static_cast<int>(cluster_rank()) : 0;
   Header* h = reinterpret_cast<Header*>(smem);
-  char* data = smem + kHeaderBytes;
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
-  // ---- this CTA's slice into shared memory, at the same offset from a
-  // 16-byte boundary as in global memory; what the first and last vector hold
-  // beside it is -inf, a masked token.  Every warp copies its own run.
-  const int64_t e0 = static_cast<int64_t>(rank) * a.L;
-  const int n = static_cast<int>(max(static_cast<int64_t>(0),
-                                     min(static_cast<int64_t>(a.L), a.V - e0)));
-  const char* src = a.logits + row * a.row_bytes + e0 * ES;
-  const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
-  const int bytes = lead + n * ES;
-  const int nvec = n > 0 ? (bytes + 15) / 16 : 0;
   Row<ES> R;
-  R.h = h, R.data = reinterpret_cast<const uint4*>(data);
-  const int run = (nvec + kWarps - 1) / kWarps;
-  R.v_first = min(nvec, warp * run), R.v_last = min(nvec, R.v_first + run);
-  R.first = static_cast<int>(e0) - lead / ES;
-  R.begin = static_cast<int>(e0), R.end = static_cast<int>(e0) + n;
-  R.C = a.C, R.rank = rank;
-  const uint32_t bar = smem_addr(&h->bar[warp]);
-  const int b0 = max(R.v_first * 16, lead > 0 ? 16 : 0), b1 = min(R.v_last * 16, bytes / 16 * 16);
-  bool timed_out = false;
-  if (lane == 0 && b1 > b0) {
-    mbar_init(bar, 1);
-    fence_mbar_init();
-    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(b1 - b0));
-    bulk_g2s(smem_addr(data + b0), src - lead + b0, static_cast<uint32_t>(b1 - b0), bar);
-  }
-  if (R.v_last > R.v_first && lane < 2 * N) {
-    const int vec = lane < N ? 0 : nvec - 1;  // the first vector, and the last
-    const bool whole = lane < N ? lead == 0 : bytes % 16 == 0 || (vec == 0 && lead > 0);
-    if (!whole && vec >= R.v_first && vec < R.v_last) {
-      const int at = vec * 16 + (lane % N) * ES;
-      const bool in = at >= lead && at < bytes;
-      if constexpr (ES == 2)
-        *reinterpret_cast<uint16_t*>(data + at) =
-            in ? *reinterpret_cast<const uint16_t*>(src - lead + at) : 0xff80u;
-      else
-        *reinterpret_cast<float*>(data + at) =
-            in ? *reinterpret_cast<const float*>(src - lead + at) : -kInf;
-    }
-  }
+  const char* src = a.logits + row * a.row_bytes;
+  R.h = h, R.stat = reinterpret_cast<float2*>(smem + kHeaderBytes);
+  R.lead = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / ES;
+  R.base = src - R.lead * ES;
+  R.V = a.V, R.G = a.G, R.C = a.C, R.rank = rank;
+  R.nvec = (R.lead + a.V + N - 1) / N;
+  R.v0 = min(R.nvec, rank * a.slice), R.v1 = min(R.nvec, R.v0 + a.slice);
+  const int groups = (R.nvec + a.G - 1) / a.G;
 
   // ---- the row's settings
   const float T = a.temperature != nullptr ? a.temperature[row] : 1.0f;
@@ -505,285 +596,261 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs a) {
   if (T == 0.0f) top_k = 1, top_p = 1.0f, min_p = 0.0f;  // the best token alone
   if (top_k >= a.V) top_k = 0;
   R.sc = T == 0.0f ? 1.0f : fminf(1.4426950408889634f / T, 3.0e38f);
-  if (tid == 0) h->count = 0;
-  __syncwarp();
-  if (b1 > b0) mbar_wait(bar, 0, timed_out);
-  __syncwarp();
+  const bool use_k = top_k > 0, use_p = top_p < 1.0f, filtered = use_k || use_p || min_p > 0.0f;
+  const bool need_mass = !use_k && (use_p || !filtered);
+  if (tid == 0) h->count = 0, h->groups = 0;
 
-  // ---- maximum (NaN wins) and seeds
-  float mx = -kInf;
-  if constexpr (ES == 2) {
-    uint32_t m = 0xff80ff80u;
-#pragma unroll 4
-    for (int i = R.v_first + lane; i < R.v_last; i += 32) {
-      const uint4 v = R.data[i];
-      m = bf16x2_max_nan(bf16x2_max_nan(m, bf16x2_max_nan(v.x, v.y)), bf16x2_max_nan(v.z, v.w));
+  // ---- one pass: every group's largest logit (NaN wins) and mass
+  bool joined = false;
+  R.each([&](int i, const uint4& raw) {
+    float m;
+    if constexpr (ES == 2) {
+      const uint32_t p = bf16x2_max_nan(bf16x2_max_nan(raw.x, raw.y), bf16x2_max_nan(raw.z, raw.w));
+      m = fmax_nan(bf16lo(p), bf16hi(p));
+    } else {
+      const Vec<4> x(raw);
+      m = fmax_nan(fmax_nan(x.x[0], x.x[1]), fmax_nan(x.x[2], x.x[3]));
     }
-    mx = fmax_nan(bf16lo(m), bf16hi(m));
-  } else {
-#pragma unroll 4
-    for (int i = R.v_first + lane; i < R.v_last; i += 32) {
-      const Vec<ES> v(R.data[i]);
-      mx = fmax_nan(mx, fmax_nan(fmax_nan(v.x[0], v.x[1]), fmax_nan(v.x[2], v.x[3])));
+    if (a.G == 32) {
+      m = float_of<4>(__reduce_max_sync(~0u, key_of<4>(m)));
+    } else {
+      for (int d = 1; d < a.G; d <<= 1) m = fmax_nan(m, __shfl_xor_sync(~0u, m, d));
     }
-  }
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the row runs
-  {
-    // the warp's largest lane maxima (upper 16 bits of their keys: a bar may be
-    // lower than the seed, never higher), 256 / (8 C) of them, to every CTA
-    uint32_t key = key_of<4>(mx) >> 16 << 16 | lane;
-    const int per = kSeeds / kWarps / a.C;
-    uint32_t mine = 0;
-    for (int j = 0; j < per; ++j) {
-      const uint32_t top = __reduce_max_sync(~0u, key);
-      if (lane == j) mine = top;
-      if (key == top) key = 0;
+    float s = 0;
+    if (need_mass) {
+      const Vec<ES> x(raw);
+      const float ref = m == -kInf ? 0.0f : m;
+#pragma unroll
+      for (int e = 0; e < N; ++e) s += weight_of(x.x[e], ref, R.sc);
+      for (int d = 1; d < a.G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
     }
-    for (int r = 0; r < a.C && lane < per; ++r) {
-      uint32_t peer;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                   : "=r"(peer)
-                   : "r"(smem_addr(&h->seed[(rank * kWarps + warp) * per + lane])), "r"(r));
-      asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(peer),
-                   "h"(static_cast<uint16_t>(mine >> 16))
+    if (!joined) {  // every CTA of the row runs: rank 0's memory can be written
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      joined = true;
+    }
+    if (lane % a.G == 0 && i < R.v1)
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                       peer_addr(R.stat + i / a.G, 0)),
+                   "f"(m), "f"(s)
                    : "memory");
-    }
+  });
+  if (!joined) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_sync();
+
+  // ---- rank 0 decides
+  float bar_x = -kInf, list_mass = 0.0f, row_mass = 0.0f;
+  int listed = 0;
+  bool more = false;
+  if (rank == 0) {
+    float mx = -kInf;
+    for (int g = tid; g < groups; g += kThreads) mx = fmax_nan(mx, R.stat[g].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mx = fmax_nan(mx, __shfl_xor_sync(~0u, mx, d));
-    if (lane == 0) h->part[warp][0] = make_float4(mx, timed_out ? 1.0f : 0.0f, 0, 0);
+    if (lane == 0) h->part[warp][0].x = mx;
     __syncthreads();
-    float late = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmax_nan(mx, h->part[w][0].x), late += h->part[w][0].y;
-    const float4(*s)[2] = R.exchange(make_float4(mx, late, 0, 0), make_float4(0, 0, 0, 0));
-    for (int r = 0; r < a.C; ++r) {
-      mx = fmax_nan(mx, s[r][0].x);
-      if (s[r][0].y != 0.0f) err |= SV_DEVERR_TIMEOUT;
-    }
-  }
-  if (!(mx > -kInf && mx < kInf)) err |= SV_DEVERR_NAN;
-  if (err != 0) {  // the same in every CTA of the row
-    if (rank == 0 && tid == 0) {
-      a.out_tokens[row] = -1;
-      if (a.out_probs != nullptr) a.out_probs[row] = 0.0f;
-      if (a.dev_error != nullptr) atomicOr(a.dev_error, static_cast<int32_t>(err));
-    }
-    return;
-  }
-  R.best = mx;
-
-  Cut cut{-kInf, INT32_MAX, 0.0f};
-  const bool use_k = top_k > 0, use_p = top_p < 1.0f;
-  if (use_k || use_p || min_p > 0.0f) {
-    // ---- the bar and the tokens at or above it
-    float bar_x;
-    if (!use_k && !use_p) {  // min-p alone: its own bar, a little lower
-      const float y = __log2f(min_p) - 0.001f;
-      bar_x = fmaf(y, 1.0f / R.sc, mx) - fabsf(mx) * 1e-6f;
-    } else {  // the R-th largest seed, by bisection over their 16 bits
-      const int want = use_k ? min(top_k, kSeeds) : kTopPSeeds;
-      uint32_t s[kSeeds / 32];
-#pragma unroll
-      for (int j = 0; j < kSeeds / 32; ++j) s[j] = h->seed[j * 32 + lane];
-      uint32_t at = 0;
-      for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1) {
-        int c = 0;
-#pragma unroll
-        for (int j = 0; j < kSeeds / 32; ++j) c += s[j] >= (at | bit) ? 1 : 0;
-        if (__reduce_add_sync(~0u, c) >= want) at |= bit;
+    for (int w = 0; w < kWarps; ++w) mx = fmax_nan(mx, h->part[w][0].x);
+    R.best = mx;
+    if (!(mx > -kInf && mx < kInf)) err |= SV_DEVERR_NAN;
+    if (err != 0) {
+      if (tid == 0) {
+        a.out_tokens[row] = -1;
+        if (a.out_probs != nullptr) a.out_probs[row] = 0.0f;
+        if (a.dev_error != nullptr) atomicOr(a.dev_error, static_cast<int32_t>(err));
       }
-      bar_x = at <= 0x7fu ? -kInf : float_of<4>(at << 16);
-    }
-    const bool need_z = !use_k && use_p;
-    typename Row<ES>::Sums v{{0, 0, 0}, {0, 0, 0}};
-    for (int i = R.v_first + lane; i < R.v_last; i += 32) {
-      const uint4 raw = R.data[i];
-      if (need_z) {
-        const Vec<ES> x(raw);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float w = R.weight(x.x[e]);
-          v.m[0] += w;
-          if (x.x[e] >= bar_x) v.m[1] += w, R.append(x.x[e], R.first + i * N + e);
+    } else {
+      if (need_mass) {  // masses relative to the best token, and their sum
+        float s = 0;
+        for (int g = tid; g < groups; g += kThreads) {
+          const float2 x = R.stat[g];
+          const float m = x.x == -kInf ? 0.0f : x.y * R.weight(x.x);
+          R.stat[g].y = m;
+          s += m;
         }
+        s = warp_sum(s);
+        __syncthreads();
+        if (lane == 0) h->part[warp][0].x = s;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) row_mass += h->part[w][0].x;
+      }
+      if (!filtered) {
+        draw<ES>(R, a, row, groups, u, Cut{-kInf, INT32_MAX, 0.0f}, 0.0f);
       } else {
-        float top;
-        if constexpr (ES == 2) {
-          const uint32_t m = bf16x2_max_nan(bf16x2_max_nan(raw.x, raw.y), bf16x2_max_nan(raw.z, raw.w));
-          top = fmaxf(bf16lo(m), bf16hi(m));
-        } else {
-          const Vec<ES> x(raw);
-          top = fmaxf(fmaxf(x.x[0], x.x[1]), fmaxf(x.x[2], x.x[3]));
-        }
-        if (top >= bar_x) {
-          const Vec<ES> x(raw);
+        // -- the bar
+        const int want = min(use_k ? top_k : kTopPSeeds, groups);
+        if (!use_k && !use_p) {  // min-p alone: its own bar, a little lower
+          bar_x = fmaf(__log2f(min_p) - 0.001f, 1.0f / R.sc, mx) - fabsf(mx) * 1e-6f;
+        } else if (want == 1 && use_k) {
+          bar_x = mx;
+        } else if (a.V > kList) {
+          // the want-th largest group maximum, by two bits a round of the upper
+          // 16 bits of the keys: the bar may be lower than the maximum, not higher
+          uint32_t at = 0;
+          for (int shift = 14, round = 0; shift >= 0; shift -= 2, round ^= 1) {
+            int c[3] = {0, 0, 0};
+            for (int g = tid; g < groups; g += kThreads) {
+              const uint32_t k = key_of<4>(R.stat[g].x) >> 16;
 #pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (x.x[e] >= bar_x) v.m[1] += R.weight(x.x[e]), R.append(x.x[e], R.first + i * N + e);
+              for (int j = 0; j < 3; ++j) c[j] += k >= (at | static_cast<uint32_t>(j + 1) << shift) ? 1 : 0;
+            }
+            // three counts of at most 2^10 groups a warp in one word
+            const int mine = __reduce_add_sync(~0u, c[0] | c[1] << 10 | c[2] << 20);
+            if (lane == 0) h->bits[round][warp] = mine;
+            __syncthreads();
+            int t0 = 0, t1 = 0, t2 = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const int x = h->bits[round][w];
+              t0 += x & 1023, t1 += x >> 10 & 1023, t2 += x >> 20 & 1023;
+            }
+            at |= static_cast<uint32_t>(t2 >= want ? 3 : t1 >= want ? 2 : t0 >= want ? 1 : 0) << shift;
+          }
+          bar_x = at <= 0x7fu ? -kInf : float_of<4>(at << 16);
+        }
+        // -- the groups that reach it, and their tokens that do
+        int32_t* reached = h->id;  // until the list is ranked
+        __syncthreads();
+        for (int g = tid; g < groups; g += kThreads)
+          if (R.stat[g].x >= bar_x) {
+            const int at = atomicAdd(&h->groups, 1);
+            if (at < kList) reached[at] = g;
+          }
+        __syncthreads();
+        const int vecs = min(h->groups, kList) * a.G;
+        if (h->groups <= kList) {
+          for (int i0 = tid; i0 < vecs; i0 += kThreads * 4) {
+            uint4 x[4];
+            int v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int i = i0 + k * kThreads;
+              v[k] = i < vecs ? reached[i / a.G] * a.G + i % a.G : R.nvec;
+              if (v[k] < R.nvec) x[k] = R.load(v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (v[k] < R.nvec) {
+                const Vec<ES> y(x[k]);
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                  if (y.x[e] >= bar_x) {
+                    list_mass += R.weight(y.x[e]);
+                    const int id = R.token(v[k], e);
+                    if (id >= 0 && id < a.V) {
+                      const int at = atomicAdd(&h->count, 1);
+                      if (at < kList) h->all[at] = entry_of(y.x[e], id);
+                    }
+                  }
+              }
+          }
+        }
+        list_mass = warp_sum(list_mass);
+        __syncthreads();
+        if (lane == 0) h->part[warp][0].x = list_mass;
+        __syncthreads();
+        list_mass = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) list_mass += h->part[w][0].x;
+        listed = h->groups <= kList ? h->count : INT32_MAX;
+        more = listed > kList ||
+               (use_k ? top_k > listed : use_p && listed < a.V && list_mass < top_p * row_mass);
+        if (!more) {
+          // -- the cuts and the draw on the ranked list
+          R.rank_list(listed);
+          if (warp == 0) {
+            float kept, total;
+            int keep = use_k ? top_k : listed;
+            R.reach(keep, kInf, &kept);
+            if (!use_k) kept = row_mass;
+            if (use_p) keep = R.reach(keep, top_p * kept, &total);
+            if (min_p > 0.0f) {
+              int c = 0;
+              for (int i = lane; i < keep; i += 32) c += h->w[i] >= min_p ? 1 : 0;
+              keep = __reduce_add_sync(~0u, c);
+            }
+            R.reach(keep, kInf, &total);
+            if (lane == 0) h->cut = keep, h->total = total, h->pick = INT32_MAX;
+          }
+          __syncthreads();
+          const int keep = h->cut;
+          const float total = h->total, target = u * total;
+          for (int i = tid; i < keep; i += kThreads) {
+            const int id = h->id[i];
+            float c = h->w[i];
+            bool later = false;
+            for (int j = 0; j < keep; ++j) {
+              const int o = h->id[j];
+              if (o < id) c += h->w[j];
+              later |= o > id;
+            }
+            if (c > target || !later) atomicMin(&h->pick, id);
+          }
+          __syncthreads();
+          for (int i = tid; i < keep; i += kThreads)
+            if (h->id[i] == h->pick) {
+              a.out_tokens[row] = h->pick;
+              if (a.out_probs != nullptr) a.out_probs[row] = h->w[i] / total;
+            }
         }
       }
     }
-    __syncthreads();
-    // every CTA's count (at .w) beside the masses
-    v.c[0] = tid == 0 ? h->count : 0;
-    const int parity = R.parity;
-    const typename Row<ES>::Sums s = R.total(v);
-    const int listed = s.c[0];
-    const bool enough = listed <= kList && (use_k ? top_k <= listed : !use_p || s.m[1] >= top_p * s.m[0]);
-    if (enough) {
-      // ---- rank 0 finishes on the list
-      int before = 0;
-      for (int r = 0; r < rank; ++r) before += __float_as_int(h->slot[parity][r][1].x);
-      R.send(before);
-      if (rank != 0) return;
-      R.rank_list(listed);
-      if (warp == 0) {
-        float kept, total;
-        int keep = use_k ? top_k : listed;
-        R.reach(keep, kInf, &kept);
-        if (!use_k) kept = s.m[0];
-        if (use_p) keep = R.reach(keep, top_p * kept, &total);
-        if (min_p > 0.0f) {
-          int c = 0;
-          for (int i = lane; i < keep; i += 32) c += h->w[i] >= min_p ? 1 : 0;
-          keep = __reduce_add_sync(~0u, c);
-        }
-        R.reach(keep, kInf, &total);
-        if (lane == 0) h->cut = keep, h->total = total, h->pick = INT32_MAX;
-      }
-      __syncthreads();
-      const int keep = h->cut;
-      const float total = h->total, target = u * total;
-      for (int i = tid; i < keep; i += kThreads) {
-        const int id = h->id[i];
-        float c = h->w[i];
-        bool later = false;
-        for (int j = 0; j < keep; ++j) {
-          if (h->id[j] < id) c += h->w[j];
-          later |= h->id[j] > id;
-        }
-        if (c > target || !later) atomicMin(&h->pick, id);
-      }
-      __syncthreads();
-      for (int i = tid; i < keep; i += kThreads)
-        if (h->id[i] == h->pick) {
-          a.out_tokens[row] = h->pick;
-          if (a.out_probs != nullptr) a.out_probs[row] = h->w[i] / total;
-        }
-      return;
-    }
-    // ---- the cuts by search, from the bar on the side of it that they lie on
-    constexpr uint32_t kLow = ES == 2 ? 0x7fu : 0x7fffffu;  // key of -inf
-    const uint32_t bar_key = bar_x > -kInf ? key_of<ES>(bar_x) : 0, above = key_of<ES>(mx) + 1;
-    if (use_k) {
-      if (listed >= top_k && bar_key != 0)
-        cut = search<ES>(R, top_k, -1.0f, bar_key, -1, 0.0f, listed, above, 0.0f, 0);
-      else if (bar_key != 0)
-        cut = search<ES>(R, top_k, -1.0f, kLow, -1, 0.0f, a.V, bar_key, s.m[1], listed);
-      else
-        cut = search<ES>(R, top_k, -1.0f, kLow, -1, 0.0f, a.V, above, 0.0f, 0);
-      if (use_p)
-        cut = search<ES>(R, 0, top_p * cut.mass, key_of<ES>(cut.t), cut.id, cut.mass, INT32_MAX,
-                         above, 0.0f, 0);
-    } else if (use_p) {
-      const float need = top_p * s.m[0];
-      if (bar_key == 0)
-        cut = search<ES>(R, 0, need, kLow, -1, s.m[0], a.V, above, 0.0f, 0);
-      else if (s.m[1] >= need)
-        cut = search<ES>(R, 0, need, bar_key, -1, s.m[1], listed, above, 0.0f, 0);
-      else
-        cut = search<ES>(R, 0, need, kLow, -1, s.m[0], a.V, bar_key, s.m[1], listed);
-    }
+  }
+  if (!filtered) return;  // known to every CTA of the row
+
+  // ---- the verdict, and what the search starts from
+  {
+    const float4(*s)[2] = R.exchange(
+        make_float4(R.best, bar_x, list_mass, row_mass),
+        make_float4(__int_as_float(listed), __int_as_float(more ? 1 : 0), 0, 0));
+    R.best = s[0][0].x, bar_x = s[0][0].y, list_mass = s[0][0].z, row_mass = s[0][0].w;
+    listed = __float_as_int(s[0][1].x);
+    if (__float_as_int(s[0][1].y) == 0) return;
+  }
+  Cut cut{-kInf, INT32_MAX, 0.0f};
+  constexpr uint32_t kLow = ES == 2 ? 0x7fu : 0x7fffffu;  // key of -inf
+  const uint32_t above = key_of<ES>(R.best) + 1;
+  // the list's bar bounds the cut where all its tokens were counted
+  const uint32_t bar_key = bar_x > -kInf && listed != INT32_MAX ? key_of<ES>(bar_x) : 0;
+  if (use_k) {
+    if (bar_key != 0 && listed >= top_k)
+      cut = search<ES>(R, top_k, -1.0f, bar_key, -1, 0.0f, listed, above, 0.0f, 0);
+    else if (bar_key != 0)
+      cut = search<ES>(R, top_k, -1.0f, kLow, -1, 0.0f, a.V, bar_key, list_mass, listed);
+    else
+      cut = search<ES>(R, top_k, -1.0f, kLow, -1, 0.0f, a.V, above, 0.0f, 0);
+    if (use_p)
+      cut = search<ES>(R, 0, top_p * cut.mass, key_of<ES>(cut.t), cut.id, cut.mass, INT32_MAX,
+                       above, 0.0f, 0);
+  } else if (use_p) {
+    const float need = top_p * row_mass;
+    if (bar_key == 0)
+      cut = search<ES>(R, 0, need, kLow, -1, row_mass, a.V, above, 0.0f, 0);
+    else if (list_mass >= need)
+      cut = search<ES>(R, 0, need, bar_key, -1, list_mass, listed, above, 0.0f, 0);
+    else
+      cut = search<ES>(R, 0, need, kLow, -1, row_mass, a.V, bar_key, list_mass, listed);
   }
 
-  // ---- the draw: masses of the warps' runs, the run that holds u * total,
-  // and a walk along it
-  auto weight = [&](float x, int id) {
-    if (!(x > cut.t || (x == cut.t && id <= cut.id))) return 0.0f;
-    const float w = R.weight(x);
-    return w >= min_p ? w : 0.0f;
-  };
-  float m = 0;
-  for (int i = R.v_first + lane; i < R.v_last; i += 32) {
-    const Vec<ES> v(R.data[i]);
-#pragma unroll
-    for (int e = 0; e < N; ++e) m += weight(v.x[e], R.first + i * N + e);
-  }
-  m = warp_sum(m);
-  __syncthreads();
-  if (lane == 0) h->part[warp][0].x = m;
-  __syncthreads();
-  float cta = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) cta += h->part[w][0].x;
-  const float4(*s)[2] = R.exchange(make_float4(cta, 0, 0, 0), make_float4(0, 0, 0, 0));
-  float total = 0;
-  for (int r = 0; r < a.C; ++r) total += s[r][0].x;
-  const float target = u * total;
-  int owner = -1;
-  float below = 0, run_sum = 0;
-  for (int r = 0; r < a.C; ++r) {
-    const float x = s[r][0].x;
-    if (x > 0.0f) owner = r, below = run_sum;
-    run_sum += x;
-    if (x > 0.0f && run_sum > target) break;
-  }
-  if (rank != owner) return;
-  int own_warp = -1;
-  float at = below, base = below;
-  for (int w = 0; w < kWarps; ++w) {
-    const float x = h->part[w][0].x;
-    if (x > 0.0f) own_warp = w, base = at;
-    at += x;
-    if (x > 0.0f && at > target) break;
-  }
-  if (warp != own_warp) return;
-  int found = -1, last = -1;
-  float fw = 0, lw = 0, cum = base;
-  for (int i0 = R.v_first; i0 < R.v_last && found < 0; i0 += 32) {
-    const int i = i0 + lane;
-    float w[N], k = 0;
-#pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = 0;
-    if (i < R.v_last) {
-      const Vec<ES> v(R.data[i]);
-#pragma unroll
-      for (int e = 0; e < N; ++e) w[e] = weight(v.x[e], R.first + i * N + e), k += w[e];
-    }
-    float inc = k;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const float o = __shfl_up_sync(~0u, inc, d);
-      if (lane >= d) inc += o;
-    }
-    float c = cum + (inc - k);
-    int mine_id = -1, mine_last = -1;
-    float mine_w = 0, mine_lw = 0;
+  // ---- the groups' kept masses, and the draw
+  R.each([&](int i, const uint4& raw) {
+    const Vec<ES> x(raw);
+    float s = 0;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      c += w[e];
-      if (w[e] > 0.0f) {
-        mine_last = R.first + i * N + e, mine_lw = w[e];
-        if (mine_id < 0 && c > target) mine_id = mine_last, mine_w = w[e];
+      const float v = x.x[e];
+      if (v > cut.t || (v == cut.t && R.token(i, e) <= cut.id)) {
+        const float w = R.weight(v);
+        s += w >= min_p ? w : 0.0f;
       }
     }
-    const unsigned hit = __ballot_sync(~0u, mine_id >= 0);
-    const unsigned any = __ballot_sync(~0u, mine_last >= 0);
-    if (hit != 0) {
-      const int l = __ffs(hit) - 1;
-      found = __shfl_sync(~0u, mine_id, l), fw = __shfl_sync(~0u, mine_w, l);
-    }
-    if (any != 0) {
-      const int l = 31 - __clz(any);
-      last = __shfl_sync(~0u, mine_last, l), lw = __shfl_sync(~0u, mine_lw, l);
-    }
-    cum += __shfl_sync(~0u, inc, 31);
-  }
-  if (found < 0) found = last, fw = lw;  // the sums' rounding left the target past the run
-  if (lane == 0) {
-    a.out_tokens[row] = found;
-    if (a.out_probs != nullptr) a.out_probs[row] = fw / total;
-  }
+    for (int d = 1; d < a.G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
+    if (lane % a.G == 0 && i < R.v1)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(&R.stat[i / a.G].y, 0)), "f"(s)
+                   : "memory");
+  });
+  cluster_sync();
+  if (rank == 0) draw<ES>(R, a, row, groups, u, cut, min_p);
 }
 
 }  // namespace
@@ -808,16 +875,22 @@ extern "C" int spec_verify_sample(const void* logits, int64_t row_stride, int32_
     return SV_ERR_ARG;
   const int64_t row = static_cast<int64_t>(V) * es;
   if (row > SV_SAMPLE_MAX_ROW_BYTES) return SV_ERR_UNSUPPORTED;
-  // slices of at most 40 KB while eight CTAs suffice: five CTAs fit an SM, so
-  // some copy while others compute
+  Device d;
+  const int rc = device(&d);
+  if (rc != SV_OK) return rc;
+  const int per = 16 / es, vecs = (V + per - 1) / per + 1;  // one more where the row starts between
+  // CTAs a row: as many as fill the GPU at eight an SM, of at least 256 vectors
   int C = 1;
-  while (C < kMaxCluster && row > static_cast<int64_t>(C) * 40960) C *= 2;
+  while (C < kMaxCluster && 2 * static_cast<int64_t>(N) * C <= 8 * d.sms && vecs > 2 * C * 256) C *= 2;
   if (static_cast<int64_t>(N) * C > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  const int per = 16 / es;
-  const int L = ((V + C - 1) / C + per - 1) / per * per;
-  const SampleArgs a{static_cast<const char*>(logits), row_stride * es, V, C, L, temperature,
-                     top_k, top_p, min_p, uniforms, out_tokens, out_probs, dev_error};
-  const int smem = kHeaderBytes + L * es + 32;
+  const int slice = ((vecs + C - 1) / C + 31) / 32 * 32;
+  // groups of 512 bytes, or smaller ones where a row has fewer than 512 of them
+  int G = 32;
+  while (G > 1 && vecs < 512 * G) G /= 2;
+  const int stats = (vecs + G - 1) / G + 1;
+  const SampleArgs a{static_cast<const char*>(logits), row_stride * es, V, C, slice, G, stats,
+                     temperature, top_k, top_p, min_p, uniforms, out_tokens, out_probs, dev_error};
+  const int smem = kHeaderBytes + stats * 8;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return es == 2 ? launch(sample_kernel<2>, dim3(N * C), kThreads, smem, C, false, st, a)
                  : launch(sample_kernel<4>, dim3(N * C), kThreads, smem, C, false, st, a);
