@@ -34,17 +34,19 @@ namespace sv {
 namespace serve {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;      // most tokens of a list
+constexpr int kCollect = 256;   // most tokens that a search collects
+constexpr int kBins = 2048;     // of 1/64 binade of weight
 constexpr int kTopPSeeds = 192;  // group maxima that a top-p row's bar lies below
 constexpr float kInf = __builtin_huge_valf();
 
 struct SampleArgs {
   const char* logits;
   int64_t row_bytes;
-  int32_t V, C, slice, G, stats;  // CTAs a row, vectors a slice, vectors a group, most groups
+  int32_t V, C, slice, shift, stats;  // CTAs a row, vectors a slice, log2 vectors a group, most groups
   const float* temperature;
   const int32_t* top_k;
   const float *top_p, *min_p, *uniforms;
@@ -56,10 +58,16 @@ struct SampleArgs {
 struct Header {
   float4 slot[2][kMaxCluster][2];  // exchanged partials, two exchanges in turn
   float4 part[kWarps][2];
-  uint64_t all[kList];  // rank 0: the list; key above complemented id
-  float w[kList];       // rank 0: weights and ids, best first
-  int32_t id[kList];
-  int32_t bits[2][kWarps];
+  union {
+    struct {
+      uint64_t all[kList];  // rank 0: the list; key above complemented id
+      float w[kList];       // rank 0: weights and ids, best first
+      int32_t id[kList];
+    };
+    int32_t bins[kBins];  // counts of tokens by weight
+  };
+  uint64_t list[kCollect];  // this CTA's part of what a search collects
+  uint64_t sum[kWarps];
   int32_t count, pick, cut, group, groups;
   float kept, total, base;
   int32_t verdict;  // 0: done, 1: search
@@ -169,22 +177,40 @@ struct Row {
     return x.v;
   }
 
-  // f(vector index, vector, valid) over this CTA's vectors: a warp 32 together,
-  // four loads in flight; every lane takes part in every call.
+  // Vectors i0 + lane, i0 + kThreads + lane, .. of this CTA's slice.  Whole
+  // vectors of the row are loaded without a branch; its first and last one and
+  // what lies past the slice (-inf) are put right after.
+  static constexpr int kLoads = 4;
+  __device__ __forceinline__ void fetch(int i0, uint4* x) const {
+    const int in0 = lead > 0 ? 1 : 0, in1 = (lead + V) / N, i = i0 + (threadIdx.x & 31);
+    const uint4* p = reinterpret_cast<const uint4*>(base);
+    const uint32_t pad = ES == 2 ? 0xff80ff80u : 0xff800000u;
+    if (in1 > in0) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        x[k] = __ldg(p + max(min(i + k * kThreads, min(in1, v1) - 1), in0));
+    }
+    if (i0 < in0 || i0 + (kLoads - 1) * kThreads + 32 > min(in1, v1)) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int j = i + k * kThreads;
+        if (j >= v1) x[k] = make_uint4(pad, pad, pad, pad);
+        else if (j < in0 || j >= in1) x[k] = load(j);
+      }
+    }
+  }
+  __device__ __forceinline__ int start() const { return v0 + (threadIdx.x >> 5) * 32; }
+
+  // f(vector index, vector) over this CTA's vectors: a warp 32 together; every
+  // lane takes part in every call.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i0 = v0 + warp * 32; i0 < v1; i0 += kThreads * 4) {
-      uint4 x[4];
+    for (int i0 = start(); i0 < v1; i0 += kThreads * kLoads) {
+      uint4 x[kLoads];
+      fetch(i0, x);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * kThreads + lane;
-        const uint32_t pad = ES == 2 ? 0xff80ff80u : 0xff800000u;
-        x[k] = i < v1 ? load(i) : make_uint4(pad, pad, pad, pad);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k * kThreads < v1) f(i0 + k * kThreads + lane, x[k]);
+      for (int k = 0; k < kLoads; ++k)
+        if (i0 + k * kThreads < v1) f(i0 + k * kThreads + static_cast<int>(threadIdx.x & 31), x[k]);
     }
   }
 
@@ -251,33 +277,44 @@ struct Row {
         if (x.x[e] >= low) {
           const float w = weight(x.x[e]);
 #pragma unroll
-          for (int j = 0; j < 3; ++j)
-            if (x.x[e] >= t[j]) v.m[j] += w, ++v.c[j];
+          for (int j = 0; j < 3; ++j) {
+            const bool on = x.x[e] >= t[j];
+            v.m[j] += on ? w : 0.0f, v.c[j] += on ? 1 : 0;
+          }
         }
     });
     return total(v);
   }
 
-  // Into rank 0's list, from any CTA of the row.
+  // Into this CTA's list.
   __device__ __forceinline__ void append(float x, int id) {
-    if (id < 0 || id >= V) return;
-    int at;
-    asm volatile("atom.relaxed.cluster.shared::cluster.add.s32 %0, [%1], 1;"
-                 : "=r"(at)
-                 : "r"(peer_addr(&h->count, 0))
-                 : "memory");
-    if (at < kList)
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_addr(h->all, 0) + at * 8),
-                   "l"(entry_of(x, id))
+    const int at = atomicAdd(&h->count, 1);
+    if (at < kCollect) h->list[at] = entry_of(x, id);
+  }
+  // This CTA's list behind those of the ranks before it in rank 0's (`before`
+  // tokens).
+  __device__ __forceinline__ void send(int before) {
+    const int n = h->count;
+    const uint32_t peer = peer_addr(h->all, 0);
+    for (int i = threadIdx.x; i < n; i += kThreads)
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer + (before + i) * 8), "l"(h->list[i])
                    : "memory");
+    cluster_sync();
   }
 
   // Rank 0: weights and ids of the n listed tokens, best first.
   __device__ __forceinline__ void rank_list(int n) {
+    if (threadIdx.x < 4 && n + threadIdx.x < kList) h->all[n + threadIdx.x] = 0;  // below any token
+    __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const uint64_t e = h->all[i];
       int r = 0;
-      for (int j = 0; j < n; ++j) r += h->all[j] > e ? 1 : 0;
+      const ulonglong2* all = reinterpret_cast<const ulonglong2*>(h->all);
+#pragma unroll 2
+      for (int j = 0; j < n; j += 4) {
+        const ulonglong2 x = all[j / 2], y = all[j / 2 + 1];
+        r += (x.x > e ? 1 : 0) + (x.y > e ? 1 : 0) + (y.x > e ? 1 : 0) + (y.y > e ? 1 : 0);
+      }
       h->w[r] = weight(value_of(e));
       h->id[r] = id_of(e);
     }
@@ -317,18 +354,161 @@ struct Cut {
   float t;
   int id;
   float mass;
+  int parity = 0;   // of the row's next exchange
+  bool ok = true;
 };
+
+// The cut at the k-th best token (need < 0), or where the mass reaches `need`,
+// among the tokens up to `within`: the tokens below top_x counted by 1/64 binade
+// of weight (one pass), the bins around the cut collected and ranked (another).
+// Tokens at or above top_x (infinite: none) number c_top, with mass m_top; the
+// cut does not lie below floor_x.  The
+// bins' masses are estimates (count times middle weight), the masses that decide
+// are sums; not ok if the cut lies outside what was collected.
+template <int ES>
+__device__ __noinline__ Cut cut_by_bins(Row<ES> R, int k, float need, Cut within, float top_x,
+                                        float m_top, int c_top, float floor_x) {
+  constexpr int N = 16 / ES, kPer = kBins / kThreads;
+  const bool by_mass = need >= 0.0f;
+  Header* h = R.h;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float origin = top_x < kInf ? top_x : R.best, step = R.sc * 64.0f;
+  auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>((origin - x) * step)); };
+  const float low = fmaxf(floor_x, within.t);
+  const bool ties = within.id != INT32_MAX;  // of tokens at within.t only some count
+  auto inside = [&](float x, int id) {
+    return (x < top_x) & (x >= low) & (x > -kInf) & (!ties | (x > within.t) | (id <= within.id));
+  };
+  for (int i = tid; i < kBins; i += kThreads) h->bins[i] = 0;
+  __syncthreads();
+  R.each([&](int i, const uint4& raw) {
+    const Vec<ES> x(raw);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (inside(x.x[e], R.token(i, e))) atomicAdd(&h->bins[bin_of(x.x[e])], 1);
+  });
+  cluster_sync();
+  int first = 0, end = 0;  // bins to collect
+  if (R.rank == 0) {
+    static_assert(kPer == 4, "one 16-byte load a thread and rank");
+    int4 x[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < R.C)
+        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[r].x), "=r"(x[r].y), "=r"(x[r].z), "=r"(x[r].w)
+                     : "r"(peer_addr(&h->bins[tid * kPer], r)));
+    int n[kPer] = {0, 0, 0, 0};
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < R.C) n[0] += x[r].x, n[1] += x[r].y, n[2] += x[r].z, n[3] += x[r].w;
+    const float w0 = R.weight(origin);
+    float mass[kPer], m = 0;
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      mass[j] = static_cast<float>(n[j]) * w0 * ex2(-(tid * kPer + j + 0.5f) / 64.0f);
+      m += mass[j], c += n[j];
+    }
+    float mi = m;
+    int ci = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const float om = __shfl_up_sync(~0u, mi, d);
+      const int oc = __shfl_up_sync(~0u, ci, d);
+      if (lane >= d) mi += om, ci += oc;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) h->bins[tid * kPer + j] = n[j];
+    if (lane == 31) h->part[warp][0] = make_float4(mi, __int_as_float(ci), 0, 0);
+    if (tid == 0) h->cut = kBins;
+    __syncthreads();
+    mi += m_top, ci += c_top;
+    for (int w = 0; w < warp; ++w) mi += h->part[w][0].x, ci += __float_as_int(h->part[w][0].y);
+    mi -= m, ci -= c;  // before this thread's bins
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      mi += mass[j], ci += n[j];
+      if (n[j] > 0 && (by_mass ? mi >= need : ci >= k)) {
+        atomicMin(&h->cut, tid * kPer + j);
+        break;
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {  // the cut's bin and its neighbours, while a list holds them
+      int b = h->cut, lo = b, hi = b + 1, total = b < kBins - 1 ? h->bins[b] : kCollect + 1;
+      for (int j = 0; j < 4 && total <= kCollect; ++j) {
+        if (hi < kBins - 1 && total + h->bins[hi] <= kCollect) total += h->bins[hi++];
+        if (lo > 0 && total + h->bins[lo - 1] <= kCollect) total += h->bins[--lo];
+      }
+      if (total > kCollect) lo = hi = 0;
+      h->group = lo, h->groups = hi;
+    }
+    __syncthreads();
+    first = h->group, end = h->groups;
+  }
+  __syncthreads();
+  if (tid == 0) h->count = 0;
+  {
+    const float4(*s)[2] = R.exchange(make_float4(__int_as_float(first), __int_as_float(end), 0, 0),
+                                     make_float4(0, 0, 0, 0));
+    first = __float_as_int(s[0][0].x), end = __float_as_int(s[0][0].y);
+  }
+  Cut cut{0.0f, -1, 0.0f, R.parity, false};
+  if (end == 0) return cut;
+  typename Row<ES>::Sums v{{0, 0, 0}, {0, 0, 0}};  // mass and count above the collected bins
+  R.each([&](int i, const uint4& raw) {
+    const Vec<ES> x(raw);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (inside(x.x[e], R.token(i, e))) {
+        const int b = bin_of(x.x[e]);
+        if (b < first) v.m[0] += R.weight(x.x[e]), ++v.c[0];
+        else if (b < end) R.append(x.x[e], R.token(i, e));
+      }
+  });
+  __syncthreads();
+  v.c[1] = tid == 0 ? h->count : 0;
+  const int turn = R.parity;
+  const typename Row<ES>::Sums s = R.total(v);
+  int before = 0;
+  for (int r = 0; r < R.rank; ++r) before += __float_as_int(h->slot[turn][r][1].y);
+  R.send(before);
+  if (R.rank == 0) {
+    const int n = s.c[1];
+    const float above = m_top + s.m[0];
+    R.rank_list(n);
+    if (warp == 0) {
+      float sum;
+      const int want = by_mass ? n : k - c_top - s.c[0];
+      const int at = R.reach(min(n, max(want, 1)), by_mass ? need - above : kInf, &sum);
+      // the cut is here if something of it was left, and there was enough
+      const bool ok = by_mass ? need > above && above + sum >= need : want >= 1 && want <= n;
+      if (lane == 0) h->pick = ok ? h->id[at - 1] : -1, h->kept = above + sum;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads)
+      if (id_of(h->all[i]) == h->pick) h->total = value_of(h->all[i]);
+    __syncthreads();
+  }
+  const float4(*f)[2] = R.exchange(make_float4(h->total, __int_as_float(h->pick), h->kept, 0),
+                                   make_float4(0, 0, 0, 0));
+  cut.t = f[0][0].x, cut.id = __float_as_int(f[0][0].y), cut.mass = f[0][0].z;
+  cut.parity = R.parity, cut.ok = cut.id >= 0;
+  return cut;
+}
 
 // The cut at the k-th best token (need < 0), or where the mass reaches `need`,
 // within the tokens at or above key `lo` (of which ties at its value only up
 // to id `lo_id`); f_lo >= target > 0 there.  above: a value with fewer than k
 // tokens, or less mass than need, at or above it, their count and mass.
 template <int ES>
-__device__ __noinline__ Cut search(Row<ES>& R, int k, float need, uint32_t lo, int lo_id, float m_lo, int c_lo,
-                      uint32_t hi, float m_hi, int c_hi) {
+__device__ __noinline__ Cut search(Row<ES> R, int k, float need, uint32_t lo, int lo_id,
+                                   float m_lo, int c_lo, uint32_t hi, float m_hi, int c_hi) {
   const bool by_mass = need >= 0.0f;
   constexpr uint32_t kLow = ES == 2 ? 0x7fu : 0x7fffffu;  // key of -inf
-  for (int iter = 0; hi - lo > 1 && c_lo - c_hi > kList; ++iter) {
+  for (int iter = 0; hi - lo > 1 && c_lo - c_hi > kCollect; ++iter) {
     const float xh = fminf(float_of<ES>(hi), R.best), xl = float_of<ES>(lo);
     uint32_t p[3];
     if (iter < 8 && lo == kLow) {  // no lower end yet: steps of some binades of weight
@@ -369,18 +549,28 @@ __device__ __noinline__ Cut search(Row<ES>& R, int k, float need, uint32_t lo, i
   const float tl = float_of<ES>(lo), th = float_of<ES>(hi);
   const bool top = hi > key_of<ES>(R.best);  // nothing lies above
   Cut cut;
-  if (c_lo - c_hi <= kList) {  // the few tokens of the interval, ranked
+  if (c_lo - c_hi <= kCollect) {  // the few tokens of the interval, ranked
+    __syncthreads();
     if (tid == 0) h->count = 0;
-    cluster_sync();
+    __syncthreads();
     R.each([&](int i, const uint4& raw) {
       const Vec<ES> v(raw);
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (v.x[e] >= tl && (top || v.x[e] < th)) R.append(v.x[e], R.token(i, e));
+      for (int e = 0; e < N; ++e) {
+        const int id = R.token(i, e);
+        if ((v.x[e] >= tl) & (top | (v.x[e] < th)) & (id >= 0) & (id < R.V)) R.append(v.x[e], id);
+      }
     });
-    cluster_sync();
+    __syncthreads();
+    const float4(*s)[2] = R.exchange(make_float4(__int_as_float(h->count), 0, 0, 0),
+                                     make_float4(0, 0, 0, 0));
+    int before = 0, n = 0;
+    for (int r = 0; r < R.C; ++r) {
+      if (r < R.rank) before += __float_as_int(s[r][0].x);
+      n += __float_as_int(s[r][0].x);
+    }
+    R.send(before);
     if (R.rank == 0) {
-      const int n = min(h->count, kList);
       R.rank_list(n);
       if (warp == 0) {
         float sum;
@@ -474,6 +664,7 @@ __device__ __noinline__ Cut search(Row<ES>& R, int k, float need, uint32_t lo, i
         if (__float_as_int(f[r][0].x) >= 0) cut.id = __float_as_int(f[r][0].x);
   }
   if (lo_id >= 0 && cut.t == tl && cut.id > lo_id) cut.id = lo_id;
+  cut.parity = R.parity;
   return cut;
 }
 
@@ -565,7 +756,7 @@ __device__ __forceinline__ void draw(Row<ES>& R, const SampleArgs& a, int row, i
 }
 
 template <int ES>
-__global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(128) char smem[];
   constexpr int N = 16 / ES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -578,10 +769,15 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
   R.h = h, R.stat = reinterpret_cast<float2*>(smem + kHeaderBytes);
   R.lead = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / ES;
   R.base = src - R.lead * ES;
-  R.V = a.V, R.G = a.G, R.C = a.C, R.rank = rank;
+  R.V = a.V, R.G = 1 << a.shift, R.C = a.C, R.rank = rank;
   R.nvec = (R.lead + a.V + N - 1) / N;
   R.v0 = min(R.nvec, rank * a.slice), R.v1 = min(R.nvec, R.v0 + a.slice);
-  const int groups = (R.nvec + a.G - 1) / a.G;
+  const int G = R.G, groups = (R.nvec + G - 1) >> a.shift;
+
+  // ---- the first loads are on their way while the settings arrive
+  const int i_first = R.start();
+  uint4 ahead[Row<ES>::kLoads];
+  if (i_first < R.v1) R.fetch(i_first, ahead);
 
   // ---- the row's settings
   const float T = a.temperature != nullptr ? a.temperature[row] : 1.0f;
@@ -602,7 +798,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
 
   // ---- one pass: every group's largest logit (NaN wins) and mass
   bool joined = false;
-  R.each([&](int i, const uint4& raw) {
+  auto group = [&](int i, const uint4& raw) {
     float m;
     if constexpr (ES == 2) {
       const uint32_t p = bf16x2_max_nan(bf16x2_max_nan(raw.x, raw.y), bf16x2_max_nan(raw.z, raw.w));
@@ -611,10 +807,10 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
       const Vec<4> x(raw);
       m = fmax_nan(fmax_nan(x.x[0], x.x[1]), fmax_nan(x.x[2], x.x[3]));
     }
-    if (a.G == 32) {
+    if (G == 32) {
       m = float_of<4>(__reduce_max_sync(~0u, key_of<4>(m)));
     } else {
-      for (int d = 1; d < a.G; d <<= 1) m = fmax_nan(m, __shfl_xor_sync(~0u, m, d));
+      for (int d = 1; d < G; d <<= 1) m = fmax_nan(m, __shfl_xor_sync(~0u, m, d));
     }
     float s = 0;
     if (need_mass) {
@@ -622,18 +818,27 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
       const float ref = m == -kInf ? 0.0f : m;
 #pragma unroll
       for (int e = 0; e < N; ++e) s += weight_of(x.x[e], ref, R.sc);
-      for (int d = 1; d < a.G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
+      for (int d = 1; d < G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
     }
     if (!joined) {  // every CTA of the row runs: rank 0's memory can be written
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       joined = true;
     }
-    if (lane % a.G == 0 && i < R.v1)
+    if ((lane & (G - 1)) == 0 && i < R.v1)
       asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
-                       peer_addr(R.stat + i / a.G, 0)),
+                       peer_addr(R.stat + (i >> a.shift), 0)),
                    "f"(m), "f"(s)
                    : "memory");
-  });
+  };
+  for (int i0 = i_first; i0 < R.v1; i0 += kThreads * Row<ES>::kLoads) {
+    uint4 x[Row<ES>::kLoads];
+#pragma unroll
+    for (int k = 0; k < Row<ES>::kLoads; ++k) x[k] = ahead[k];
+    if (i0 + kThreads * Row<ES>::kLoads < R.v1) R.fetch(i0 + kThreads * Row<ES>::kLoads, ahead);
+#pragma unroll
+    for (int k = 0; k < Row<ES>::kLoads; ++k)
+      if (i0 + k * kThreads < R.v1) group(i0 + k * kThreads + lane, x[k]);
+  }
   if (!joined) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   cluster_sync();
 
@@ -644,6 +849,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
   if (rank == 0) {
     float mx = -kInf;
     for (int g = tid; g < groups; g += kThreads) mx = fmax_nan(mx, R.stat[g].x);
+    const float own = mx;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mx = fmax_nan(mx, __shfl_xor_sync(~0u, mx, d));
     if (lane == 0) h->part[warp][0].x = mx;
@@ -678,34 +884,18 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
         draw<ES>(R, a, row, groups, u, Cut{-kInf, INT32_MAX, 0.0f}, 0.0f);
       } else {
         // -- the bar
-        const int want = min(use_k ? top_k : kTopPSeeds, groups);
+        const int want = min(use_k ? top_k : kTopPSeeds, min(groups, kThreads));
         if (!use_k && !use_p) {  // min-p alone: its own bar, a little lower
           bar_x = fmaf(__log2f(min_p) - 0.001f, 1.0f / R.sc, mx) - fabsf(mx) * 1e-6f;
         } else if (want == 1 && use_k) {
           bar_x = mx;
         } else if (a.V > kList) {
-          // the want-th largest group maximum, by two bits a round of the upper
-          // 16 bits of the keys: the bar may be lower than the maximum, not higher
+          // the want-th largest of the threads' maxima over their groups, by the
+          // upper 16 bits of the keys: the bar may be lower than it, not higher
+          const uint32_t seed = key_of<4>(own) >> 16;
           uint32_t at = 0;
-          for (int shift = 14, round = 0; shift >= 0; shift -= 2, round ^= 1) {
-            int c[3] = {0, 0, 0};
-            for (int g = tid; g < groups; g += kThreads) {
-              const uint32_t k = key_of<4>(R.stat[g].x) >> 16;
-#pragma unroll
-              for (int j = 0; j < 3; ++j) c[j] += k >= (at | static_cast<uint32_t>(j + 1) << shift) ? 1 : 0;
-            }
-            // three counts of at most 2^10 groups a warp in one word
-            const int mine = __reduce_add_sync(~0u, c[0] | c[1] << 10 | c[2] << 20);
-            if (lane == 0) h->bits[round][warp] = mine;
-            __syncthreads();
-            int t0 = 0, t1 = 0, t2 = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              const int x = h->bits[round][w];
-              t0 += x & 1023, t1 += x >> 10 & 1023, t2 += x >> 20 & 1023;
-            }
-            at |= static_cast<uint32_t>(t2 >= want ? 3 : t1 >= want ? 2 : t0 >= want ? 1 : 0) << shift;
-          }
+          for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1)
+            if (__syncthreads_count(seed >= (at | bit)) >= want) at |= bit;
           bar_x = at <= 0x7fu ? -kInf : float_of<4>(at << 16);
         }
         // -- the groups that reach it, and their tokens that do
@@ -717,17 +907,26 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
             if (at < kList) reached[at] = g;
           }
         __syncthreads();
-        const int vecs = min(h->groups, kList) * a.G;
+        const int vecs = min(h->groups, kList) << a.shift;
+        uint64_t sum = 0;  // in 2^-40: the groups' order in the list changes nothing
         if (h->groups <= kList) {
+          const int in0 = R.lead > 0 ? 1 : 0, in1 = (R.lead + a.V) / N;
           for (int i0 = tid; i0 < vecs; i0 += kThreads * 4) {
             uint4 x[4];
             int v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int i = i0 + k * kThreads;
-              v[k] = i < vecs ? reached[i / a.G] * a.G + i % a.G : R.nvec;
-              if (v[k] < R.nvec) x[k] = R.load(v[k]);
+              v[k] = i < vecs ? (reached[i >> a.shift] << a.shift) + (i & (G - 1)) : R.nvec;
             }
+            if (in1 > in0) {  // whole vectors first, without a branch
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                x[k] = __ldg(reinterpret_cast<const uint4*>(R.base) + max(min(v[k], in1 - 1), in0));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (v[k] < R.nvec && (v[k] < in0 || v[k] >= in1)) x[k] = R.load(v[k]);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (v[k] < R.nvec) {
@@ -735,7 +934,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
 #pragma unroll
                 for (int e = 0; e < N; ++e)
                   if (y.x[e] >= bar_x) {
-                    list_mass += R.weight(y.x[e]);
+                    sum += static_cast<uint64_t>(R.weight(y.x[e]) * 0x1p40f);
                     const int id = R.token(v[k], e);
                     if (id >= 0 && id < a.V) {
                       const int at = atomicAdd(&h->count, 1);
@@ -745,13 +944,14 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
               }
           }
         }
-        list_mass = warp_sum(list_mass);
-        __syncthreads();
-        if (lane == 0) h->part[warp][0].x = list_mass;
-        __syncthreads();
-        list_mass = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) list_mass += h->part[w][0].x;
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        if (lane == 0) h->sum[warp] = sum;
+        __syncthreads();
+        sum = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += h->sum[w];
+        list_mass = static_cast<float>(sum) * 0x1p-40f;
         listed = h->groups <= kList ? h->count : INT32_MAX;
         more = listed > kList ||
                (use_k ? top_k > listed : use_p && listed < a.V && list_mass < top_p * row_mass);
@@ -779,9 +979,11 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
             const int id = h->id[i];
             float c = h->w[i];
             bool later = false;
+#pragma unroll 4
             for (int j = 0; j < keep; ++j) {
               const int o = h->id[j];
-              if (o < id) c += h->w[j];
+              const float w = h->w[j];
+              c += o < id ? w : 0.0f;
               later |= o > id;
             }
             if (c > target || !later) atomicMin(&h->pick, id);
@@ -812,24 +1014,36 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
   const uint32_t above = key_of<ES>(R.best) + 1;
   // the list's bar bounds the cut where all its tokens were counted
   const uint32_t bar_key = bar_x > -kInf && listed != INT32_MAX ? key_of<ES>(bar_x) : 0;
-  if (use_k) {
-    if (bar_key != 0 && listed >= top_k)
-      cut = search<ES>(R, top_k, -1.0f, bar_key, -1, 0.0f, listed, above, 0.0f, 0);
-    else if (bar_key != 0)
-      cut = search<ES>(R, top_k, -1.0f, kLow, -1, 0.0f, a.V, bar_key, list_mass, listed);
-    else
-      cut = search<ES>(R, top_k, -1.0f, kLow, -1, 0.0f, a.V, above, 0.0f, 0);
-    if (use_p)
-      cut = search<ES>(R, 0, top_p * cut.mass, key_of<ES>(cut.t), cut.id, cut.mass, INT32_MAX,
-                       above, 0.0f, 0);
-  } else if (use_p) {
-    const float need = top_p * row_mass;
-    if (bar_key == 0)
-      cut = search<ES>(R, 0, need, kLow, -1, row_mass, a.V, above, 0.0f, 0);
-    else if (list_mass >= need)
-      cut = search<ES>(R, 0, need, bar_key, -1, list_mass, listed, above, 0.0f, 0);
-    else
-      cut = search<ES>(R, 0, need, kLow, -1, row_mass, a.V, bar_key, list_mass, listed);
+  const bool counted = listed != INT32_MAX && bar_x > -kInf;  // the bar's list bounds the cut
+  const Cut all{-kInf, INT32_MAX, 0.0f};
+  if (use_k || use_p) {
+    const float need = use_k ? -1.0f : top_p * row_mass;
+    const bool below = counted && (use_k ? listed < top_k : list_mass < need);
+    const float m_top = below ? list_mass : 0.0f;
+    const int c_top = below ? listed : 0;
+    // what lies below the floor has less mass than the cut leaves, or top_k
+    // tokens are above it: the bar's, where it is that of the top_k-th seed
+    float floor_x = -kInf;
+    if (!use_k)
+      floor_x = R.best + __log2f(0.99f * (1.0f - top_p) * row_mass / a.V) / R.sc;
+    else if (top_k <= min(groups, kThreads))
+      floor_x = bar_x;
+    cut = cut_by_bins<ES>(R, top_k, need, all, below ? bar_x : kInf, m_top, c_top, floor_x);
+    R.parity = cut.parity;
+    if (!cut.ok) {
+      cut = search<ES>(R, top_k, need, kLow, -1, row_mass, a.V, below ? bar_key : above, m_top, c_top);
+      R.parity = cut.parity;
+    }
+  }
+  if (use_k && use_p) {
+    const Cut k = cut;
+    const float need = top_p * k.mass;
+    cut = cut_by_bins<ES>(R, 0, need, k, kInf, 0.0f, 0, -kInf);
+    R.parity = cut.parity;
+    if (!cut.ok) {
+      cut = search<ES>(R, 0, need, key_of<ES>(k.t), k.id, k.mass, INT32_MAX, above, 0.0f, 0);
+      R.parity = cut.parity;
+    }
   }
 
   // ---- the groups' kept masses, and the draw
@@ -838,15 +1052,13 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(const SampleArgs a)
     float s = 0;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const float v = x.x[e];
-      if (v > cut.t || (v == cut.t && R.token(i, e) <= cut.id)) {
-        const float w = R.weight(v);
-        s += w >= min_p ? w : 0.0f;
-      }
+      const float v = x.x[e], w = R.weight(v);
+      const bool on = (w >= min_p) & ((v > cut.t) | ((v == cut.t) & (R.token(i, e) <= cut.id)));
+      s += on ? w : 0.0f;
     }
-    for (int d = 1; d < a.G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
-    if (lane % a.G == 0 && i < R.v1)
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(&R.stat[i / a.G].y, 0)), "f"(s)
+    for (int d = 1; d < G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
+    if ((lane & (G - 1)) == 0 && i < R.v1)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(&R.stat[i >> a.shift].y, 0)), "f"(s)
                    : "memory");
   });
   cluster_sync();
@@ -884,11 +1096,13 @@ extern "C" int spec_verify_sample(const void* logits, int64_t row_stride, int32_
   while (C < kMaxCluster && 2 * static_cast<int64_t>(N) * C <= 8 * d.sms && vecs > 2 * C * 256) C *= 2;
   if (static_cast<int64_t>(N) * C > INT32_MAX) return SV_ERR_UNSUPPORTED;
   const int slice = ((vecs + C - 1) / C + 31) / 32 * 32;
-  // groups of 512 bytes, or smaller ones where a row has fewer than 512 of them
-  int G = 32;
-  while (G > 1 && vecs < 512 * G) G /= 2;
-  const int stats = (vecs + G - 1) / G + 1;
-  const SampleArgs a{static_cast<const char*>(logits), row_stride * es, V, C, slice, G, stats,
+  // groups of 8 vectors; more where that makes over 4096 of them, fewer where a
+  // row has fewer than 512
+  int shift = 3;
+  while (shift < 5 && vecs > 4096 << shift) ++shift;
+  while (shift > 0 && vecs < 512 << shift) --shift;
+  const int stats = (vecs >> shift) + 2;
+  const SampleArgs a{static_cast<const char*>(logits), row_stride * es, V, C, slice, shift, stats,
                      temperature, top_k, top_p, min_p, uniforms, out_tokens, out_probs, dev_error};
   const int smem = kHeaderBytes + stats * 8;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
