@@ -755,8 +755,9 @@ __device__ __forceinline__ void draw(Row<ES>& R, const SampleArgs& a, int row, i
   }
 }
 
-template <int ES>
-__global__ __launch_bounds__(kThreads, 2) void sample_kernel(const SampleArgs a) {
+// PER_SM: CTAs an SM that the registers are cut for.
+template <int ES, int PER_SM>
+__global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(128) char smem[];
   constexpr int N = 16 / ES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1091,9 +1092,12 @@ extern "C" int spec_verify_sample(const void* logits, int64_t row_stride, int32_
   const int rc = device(&d);
   if (rc != SV_OK) return rc;
   const int per = 16 / es, vecs = (V + per - 1) / per + 1;  // one more where the row starts between
-  // CTAs a row: as many as fill the GPU at eight an SM, of at least 256 vectors
-  int C = 1;
-  while (C < kMaxCluster && 2 * static_cast<int64_t>(N) * C <= 8 * d.sms && vecs > 2 * C * 256) C *= 2;
+  // CTAs a row, each of at least 512 vectors: one an SM for up to a quarter as
+  // many rows as SMs (the kernel then has 128 registers a thread; 32 rows under
+  // top-p 48 us, two an SM 55 us), else as many as fit at two an SM (96 rows:
+  // three CTAs a row 15 us, four 24 us; 512 rows: one 59 us, two 72 us).
+  const bool wide = 4 * static_cast<int64_t>(N) <= d.sms;
+  const int C = std::max(1, std::min({kMaxCluster, (wide ? 1 : 2) * d.sms / N, vecs / 512}));
   if (static_cast<int64_t>(N) * C > INT32_MAX) return SV_ERR_UNSUPPORTED;
   const int slice = ((vecs + C - 1) / C + 31) / 32 * 32;
   // groups of 8 vectors; more where that makes over 4096 of them, fewer where a
@@ -1106,6 +1110,9 @@ extern "C" int spec_verify_sample(const void* logits, int64_t row_stride, int32_
                      temperature, top_k, top_p, min_p, uniforms, out_tokens, out_probs, dev_error};
   const int smem = kHeaderBytes + stats * 8;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return es == 2 ? launch(sample_kernel<2>, dim3(N * C), kThreads, smem, C, false, st, a)
-                 : launch(sample_kernel<4>, dim3(N * C), kThreads, smem, C, false, st, a);
+  if (wide)
+    return es == 2 ? launch(sample_kernel<2, 1>, dim3(N * C), kThreads, smem, C, false, st, a)
+                   : launch(sample_kernel<4, 1>, dim3(N * C), kThreads, smem, C, false, st, a);
+  return es == 2 ? launch(sample_kernel<2, 2>, dim3(N * C), kThreads, smem, C, false, st, a)
+                 : launch(sample_kernel<4, 2>, dim3(N * C), kThreads, smem, C, false, st, a);
 }
