@@ -203,7 +203,7 @@ bool encode_cache(CUtensorMap* map, const void* base, const AttnArgs& a, int kv_
 template <int NS, int DP>
 int launch_mma(const MmaArgs& p, int grid, const CUtensorMap& km, const CUtensorMap& vm,
                cudaStream_t st) {
-  constexpr int threads = (NS * 4 + 2) * 32, smem = attn_smem(NS, DP);
+  constexpr int threads = attn_threads(NS), smem = attn_smem(NS, DP);
   int rc = p.box > 0
                ? launch(attn_mma_kernel<NS, DP, true>, dim3(grid), threads, smem, 1, false, st, p, km, vm)
                : launch(attn_mma_kernel<NS, DP, false>, dim3(grid), threads, smem, 1, false, st, p, km, vm);

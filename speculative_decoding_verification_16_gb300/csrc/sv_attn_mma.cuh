@@ -236,13 +236,23 @@ struct AttnBars {
 };
 static_assert(sizeof(AttnBars) <= 256, "barrier block");
 
+// Registers: the softmax warps hold a tile's row, the others little.  Of the
+// launch's share (NS = 1: 256 threads x 128, NS = 2: 384 x 168) the copying and
+// issuing warpgroup gives up what the softmax warpgroups take: 128 x 40 + 128 x
+// 216 = 256 x 128, and 128 x 56 + 256 x 224 = 384 x 168.
+template <int NS>
+struct AttnRegs {
+  static constexpr int kLess = NS == 1 ? 40 : 56, kMore = NS == 1 ? 216 : 224;
+};
+__host__ __device__ constexpr int attn_threads(int ns) { return (ns + 1) * 128; }
+
 template <int NS, int DP, bool TMA>
-__global__ __launch_bounds__((NS * 4 + 2) * 32, 3 - NS) void attn_mma_kernel(
+__global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
     const MmaArgs p, const __grid_constant__ CUtensorMap kmap,
     const __grid_constant__ CUtensorMap vmap) {
   using L = AttnSmem<NS, DP>;
   constexpr int MR = NS * kTile;
-  constexpr int kThreads = (NS * 4 + 2) * 32;
+  constexpr int kThreads = attn_threads(NS);
   constexpr uint32_t kCols = NS == 1 ? 256 : 512;
   // tensor memory columns: S (and P) of each stream, then O of each
   constexpr uint32_t kO = NS * kTile;
@@ -284,6 +294,8 @@ __global__ __launch_bounds__((NS * 4 + 2) * 32, 3 - NS) void attn_mma_kernel(
   auto full = [&](int u) { return smem_addr(&bars->full[u]); };
   auto empty = [&](int u) { return smem_addr(&bars->empty[u]); };
 
+  if (warp >= NS * 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AttnRegs<NS>::kLess));
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------- copies
     int u = 0;          // ring position
@@ -468,7 +480,9 @@ __global__ __launch_bounds__((NS * 4 + 2) * 32, 3 - NS) void attn_mma_kernel(
       }
     }
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AttnRegs<NS>::kMore));
     // ---------------------------------------------------------- softmax
     const int st = warp >> 2;          // stream
     const int row = tid & 127;         // row of the stream's tile
