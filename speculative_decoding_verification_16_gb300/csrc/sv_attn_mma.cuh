@@ -9,7 +9,7 @@
 // a worker whose run starts or ends inside an item leaves an unnormalised
 // partial (O, m, l) in the workspace, and the combine kernel joins them.
 //
-// Per stream of 128 rows (one softmax warpgroup, a thread a row) and key tile:
+// Per stream of 128 rows and key tile:
 //   S = Q K^T   tcgen05.mma from shared memory into 128 tensor memory columns
 //   P = 2^(S c - m c), c = scale log2 e, rounded to bf16 over S's own columns
 //   O += P V    tcgen05.mma with P from tensor memory
@@ -21,8 +21,12 @@
 // NS = 1 (at most 128 rows an item, decoding and verify steps: the cache's
 // bytes bound it): two CTAs an SM, each with one stream and a ring of 64-key
 // copies; while one's softmax runs, the other's products do.
+// One softmax warpgroup, a thread a row.
 // NS = 2 (longer chunks: the products bound it): one CTA an SM, two streams
-// over the same key/value tiles, the tensor core alternating between them.
+// over the same key/value tiles, the tensor core alternating between them: its
+// 1,024 cycles a tile for one stream are the time that the other's softmax may
+// take.  Two warpgroups a stream, a thread half a row's columns: with one, the
+// softmax took 3,400 cycles from S to P.
 //
 // Keys and values come by tensor copies of whole page pieces (page sizes that
 // are a multiple of 64 or 8, 16, 32) and by 16-byte copies of single rows
@@ -63,9 +67,14 @@ struct MmaArgs {
 };
 
 __host__ __device__ constexpr int attn_unit_tokens(int ns) { return ns == 1 ? 64 : 128; }
-__host__ __device__ constexpr int attn_units(int ns, int dp) { return dp == 128 ? 5 : ns == 1 ? 10 : 10; }
+__host__ __device__ constexpr int attn_units(int ns, int dp) { return (ns == 1 ? 5 : 4) * 128 / dp; }
+__host__ __device__ constexpr int attn_softmax_warps(int ns) { return ns == 1 ? 4 : 16; }
+__host__ __device__ constexpr int attn_threads(int ns) { return (attn_softmax_warps(ns) + 4) * 32; }
+// query tiles, ring, barriers, the softmax warps' walks, and for two warpgroups
+// a stream what they exchange
 __host__ __device__ constexpr int attn_smem(int ns, int dp) {
-  return ns * kTile * dp * 2 + attn_units(ns, dp) * attn_unit_tokens(ns) * dp * 2 + 256;
+  return ns * kTile * dp * 2 + attn_units(ns, dp) * attn_unit_tokens(ns) * dp * 2 + 256 +
+         attn_softmax_warps(ns) * 104 + (ns == 1 ? 0 : ns * 4 * kTile * 4);
 }
 
 // ---------------------------------------------------------------- work
@@ -236,15 +245,40 @@ struct AttnBars {
 };
 static_assert(sizeof(AttnBars) <= 256, "barrier block");
 
-// Registers: the softmax warps hold a tile's row, the others little.  Of the
-// launch's share (NS = 1: 256 threads x 128, NS = 2: 384 x 168) the copying and
-// issuing warpgroup gives up what the softmax warpgroups take: 128 x 40 + 128 x
-// 216 = 256 x 128, and 128 x 56 + 256 x 224 = 384 x 168.
+// Registers: the softmax warps hold their part of a tile's row, the others
+// little.  Of the launch's share (NS = 1: 256 threads x 128, NS = 2: 640 x 96)
+// the copying and issuing warpgroup gives up what the softmax warpgroups take:
+// 128 x 40 + 128 x 216 = 256 x 128, and 128 x 64 + 512 x 104 = 640 x 96.
 template <int NS>
 struct AttnRegs {
-  static constexpr int kLess = NS == 1 ? 40 : 56, kMore = NS == 1 ? 216 : 224;
+  static constexpr int kLess = NS == 1 ? 40 : 64, kMore = NS == 1 ? 216 : 104;
 };
-__host__ __device__ constexpr int attn_threads(int ns) { return (ns + 1) * 128; }
+
+// Two floats at once: a * b + c and a + b.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+template <int MR>
+struct WarpWalk {
+  Walk<MR> walk;
+  Segment next;
+};
 
 template <int NS, int DP, bool TMA>
 __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
@@ -262,7 +296,11 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   char* const ring = smem + NS * L::kQBytes;
   AttnBars* const bars = reinterpret_cast<AttnBars*>(ring + L::kUnits * L::kUnitBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kLoadWarp = NS * 4, kMmaWarp = NS * 4 + 1;
+  constexpr int kSoftmax = attn_softmax_warps(NS), kLoadWarp = kSoftmax, kMmaWarp = kSoftmax + 1;
+  constexpr int kSplit = kSoftmax / (NS * 4);  // warpgroups a stream
+  WarpWalk<MR>* const walks = reinterpret_cast<WarpWalk<MR>*>(reinterpret_cast<char*>(bars) + 256);
+  static_assert(sizeof(WarpWalk<MR>) <= 104, "walk block");
+  float* const swap = reinterpret_cast<float*>(reinterpret_cast<char*>(walks) + kSoftmax * 104);
   bool timed_out = false;
 
   Walk<MR> walk;
@@ -276,9 +314,9 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       mbar_init(smem_addr(&bars->empty[i]), 1);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_addr(&bars->q[s]), 128);
+      mbar_init(smem_addr(&bars->q[s]), 128 * kSplit);
       mbar_init(smem_addr(&bars->s[s]), 1);
-      mbar_init(smem_addr(&bars->p[s]), 128);
+      mbar_init(smem_addr(&bars->p[s]), 128 * kSplit);
       mbar_init(smem_addr(&bars->o[s]), 1);
     }
     mbar_init(smem_addr(&bars->idle), 1);
@@ -294,7 +332,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   auto full = [&](int u) { return smem_addr(&bars->full[u]); };
   auto empty = [&](int u) { return smem_addr(&bars->empty[u]); };
 
-  if (warp >= NS * 4) {
+  if (warp >= kSoftmax) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AttnRegs<NS>::kLess));
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------- copies
@@ -484,16 +522,19 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AttnRegs<NS>::kMore));
     // ---------------------------------------------------------- softmax
-    const int st = warp >> 2;          // stream
-    const int row = tid & 127;         // row of the stream's tile
-    const int wrow = (warp & 3) * 32;  // the warp's first row
+    constexpr int kCols = kTile / kSplit;   // columns of S a thread
+    constexpr int kOut = DP / kSplit;       // columns of O a thread
+    const int st = warp / (4 * kSplit);     // stream
+    const int part = (warp >> 2) % kSplit;  // columns [part * kCols, ..)
+    const int row = tid & 127;              // row of the stream's tile
+    const int wrow = (warp & 3) * 32;       // the warp's first row
     const uint32_t lanes = static_cast<uint32_t>(wrow) << 16;
-    const uint32_t s_at = tmem + lanes + st * kTile, o_at = tmem + lanes + kO + st * DP;
-    const uint32_t qdst = q_addr + st * L::kQBytes;
-    const uint32_t qbar = smem_addr(&bars->q[st]), sbar = smem_addr(&bars->s[st]),
-                   pbar = smem_addr(&bars->p[st]), obar = smem_addr(&bars->o[st]);
-    const bool neg = a.scale2 < 0.0f;
+    const uint32_t s_at = tmem + lanes + st * kTile,
+                   o_at = tmem + lanes + kO + st * DP + part * kOut;
+    const uint32_t sbar = smem_addr(&bars->s[st]), pbar = smem_addr(&bars->p[st]),
+                   obar = smem_addr(&bars->o[st]);
     const float c = fabsf(a.scale2);
+    WarpWalk<MR>* const ww = walks + warp;
     uint32_t turn = 0;  // parity of the stream's next tile
     uint32_t idle = 0;  // parity of the next segment without rows here
     int vu = 0;         // ring position of the tile's first V unit
@@ -502,42 +543,61 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       vu += n;
       if (vu >= L::kUnits) vu -= L::kUnits, vturn ^= 1;
     };
-
-    // the query rows of a segment: lane's own row address, then 16-byte pieces
-    auto load_q = [&](const Segment& g) {
-      const int i = g.m * MR + st * kTile + wrow + lane;
-      const bool on = st * kTile + wrow + lane < g.rows;
+    // x of this thread's row in the stream's other warpgroup; `slot` in turn
+    auto exchange = [&](float x, int slot) {
+      float* at = swap + (st * 2 + slot) * 2 * kTile + row;
+      at[part * kTile] = x;
+      named_bar_sync(1 + st, 256);
+      return at[(part ^ 1) * kTile];
+    };
+    // the walk's next segment, by lane 0, into shared memory (tile1 = -1: none)
+    auto advance = [&]() {
+      __syncwarp();
+      if (lane == 0) {
+        Walk<MR> w = ww->walk;
+        Segment n;
+        if (!w.next(p, &n)) n.tile1 = -1;
+        ww->walk = w;
+        ww->next = n;
+      }
+      __syncwarp();
+    };
+    // the next segment's query rows: lane's own row address, then 16-byte pieces
+    auto load_q = [&]() {
+      const Segment& n = ww->next;
+      const int i = n.m * MR + st * kTile + wrow + lane;
       const char* src = nullptr;
-      if (on)
-        src = a.q + static_cast<int64_t>(g.row0 + i / a.group) * a.q_row +
-              static_cast<int64_t>(g.h * a.group + i % a.group) * a.q_head;
+      if (st * kTile + wrow + lane < n.rows)
+        src = a.q + static_cast<int64_t>(n.row0 + i / a.group) * a.q_row +
+              static_cast<int64_t>(n.h * a.group + i % a.group) * a.q_head;
       constexpr int kPieces = DP / 8;
-      if (st * kTile + wrow < g.rows) {
+      if (st * kTile + wrow < n.rows) {
 #pragma unroll 4
-        for (int k = 0; k < kPieces; ++k) {
+        for (int k = part; k < kPieces; k += kSplit) {
           const int rr = k * 32 / kPieces + lane / kPieces, j = lane % kPieces;
           const char* from = reinterpret_cast<const char*>(
               __shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), rr));
           const bool ok = from != nullptr && j * 8 < a.dim;
-          cp_async16(qdst + (j / 8) * (kTile * 128) + (wrow + rr) * 128 + (((j & 7) ^ (rr & 7)) << 4),
+          cp_async16(q_addr + st * L::kQBytes + (j / 8) * (kTile * 128) + (wrow + rr) * 128 +
+                         (((j & 7) ^ (rr & 7)) << 4),
                      ok ? from + j * 16 : a.q, ok ? 16 : 0);
         }
       }
       cp_async_commit();
     };
 
-    Segment g, next;
-    bool more = walk.next(p, &g);
-    load_q(g);
-    while (more) {
+    if (lane == 0) ww->walk = walk;
+    __syncwarp();
+    advance();
+    load_q();
+    while (ww->next.tile1 >= 0) {
+      const Segment g = ww->next;
       cp_async_wait<0>();
       fence_async_smem();
-      mbar_arrive(qbar);
-      const bool has_next = walk.next(p, &next);
-      const bool live = st * kTile < g.rows;          // the stream has rows
-      const bool work = st * kTile + wrow < g.rows;   // the warp has rows
-      const int token = (g.m * MR + st * kTile + row) / a.group;  // of this thread's row
-      const int pos = g.seq - g.l + token;
+      mbar_arrive(smem_addr(&bars->q[st]));
+      const bool live = st * kTile < g.rows;         // the stream has rows
+      const bool work = st * kTile + wrow < g.rows;  // the warp has rows
+      const int pos = g.seq - g.l + (g.m * MR + st * kTile + row) / a.group;  // of this row
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       // keys that every row of the item sees: [all_lo, all_hi)
       const int all_hi = g.seq - g.l + g.m * MR / a.group + 1;
@@ -547,9 +607,11 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
 
       if (!live) {  // the other stream's tiles pass through the ring
         mbar_wait(smem_addr(&bars->idle), idle, timed_out);
+        __syncwarp();
         idle ^= 1;
         for (int tile = g.tile0; tile < g.tile1; ++tile) ring_step(2 * L::kPerTile);
-        if (has_next) load_q(next);
+        advance();
+        if (ww->next.tile1 >= 0) load_q();
       }
       for (int tile = g.tile0; live && tile < g.tile1; ++tile) {
         const int t0 = tile * kTile;
@@ -562,7 +624,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           for (int i = 0; i < L::kPerTile; ++i) {
             mbar_wait(full(un), ut, timed_out);
             char* unit = ring + un * L::kUnitBytes;
-            for (int at = row; at < L::kUnitBytes / 16; at += 128) {
+            for (int at = row + part * 128; at < L::kUnitBytes / 16; at += 128 * kSplit) {
               const int t = t0 + i * L::kUnitTokens + (at >> 3) % L::kUnitTokens;
               if (t >= all_lo && t < all_hi) continue;
               uint4 v = *reinterpret_cast<const uint4*>(unit + at * 16);
@@ -586,26 +648,34 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
         mbar_wait(sbar, turn, timed_out);
         __syncwarp();
         tmem_fence_after();
-        if (tile + 1 == g.tile1 && has_next) load_q(next);  // the last S is formed: Q is free
+        if (tile + 1 == g.tile1) {  // the last S is formed: the query buffer is free
+          advance();
+          if (ww->next.tile1 >= 0) load_q();
+        }
         if (work) {
-          uint32_t x[kTile];
+          uint32_t x[kCols];
 #pragma unroll
-          for (int k = 0; k < kTile; k += 32) tmem_ld32(s_at + k, x + k);
+          for (int k = 0; k < kCols; k += 32) tmem_ld32(s_at + part * kCols + k, x + k);
           tmem_wait_ld();
           float* s = reinterpret_cast<float*>(x);
-          if (neg) {
+          if (a.scale2 < 0.0f) {
 #pragma unroll
-            for (int k = 0; k < kTile; ++k) s[k] = -s[k];
+            for (int k = 0; k < kCols; ++k) s[k] = -s[k];
           }
           if (edge) {
-            const int from = lo - t0, to = pos + 1 - t0;
+            const int from = lo - t0 - part * kCols, to = pos + 1 - t0 - part * kCols;
 #pragma unroll
-            for (int k = 0; k < kTile; ++k) s[k] = k >= from && k < to ? s[k] : -kInf;
+            for (int k = 0; k < kCols; ++k) s[k] = k >= from && k < to ? s[k] : -kInf;
           }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
+          float mx[4] = {m, s[0], s[1], s[2]};
+          mx[3] = fmaxf(mx[3], s[3]);
 #pragma unroll
-          for (int k = 4; k < kTile; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
-          const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          for (int k = 4; k < kCols; k += 8)
+#pragma unroll
+            for (int e = 0; e < 4 && k + 2 * e < kCols; ++e)
+              mx[e] = fmaxf(fmaxf(mx[e], s[k + 2 * e]), s[k + 2 * e + 1]);
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if constexpr (kSplit == 2) top = fmaxf(top, exchange(top, turn));
           if (tile == g.tile0) {
             m = top;
           } else {
@@ -616,13 +686,13 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
               __syncwarp();
               tmem_fence_after();
 #pragma unroll
-              for (int k = 0; k < DP; k += 32) {
-                uint32_t o[32];
-                tmem_ld32(o_at + k, o);
+              for (int k = 0; k < kOut; k += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_at + k, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(o_at + k, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_at + k, o);
               }
               l *= f;
               m = top;
@@ -632,24 +702,30 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           if (__any_sync(~0u, fabsf(base) > 0x1p20f)) {
             // scores so large that the rounding of m c would not cancel in s c - m c
 #pragma unroll
-            for (int k = 0; k < kTile; ++k) s[k] = (s[k] - (m == -kInf ? 0.0f : m)) * c;
+            for (int k = 0; k < kCols; ++k) s[k] = (s[k] - (m == -kInf ? 0.0f : m)) * c;
             base = 0.0f, mul = 1.0f;
           }
-          float sum[4] = {0, 0, 0, 0};
+          const uint64_t mul2 = pack2(mul, mul), base2 = pack2(-base, -base);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int k = 0; k < kTile; k += 32) {
+          for (int k = 0; k < kCols; k += 32) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(fmaf(s[k + 2 * e], mul, -base));
-              const float p1 = ex2(fmaf(s[k + 2 * e + 1], mul, -base));
-              sum[e & 1] += p0, sum[2 + (e & 1)] += p1;
+              float p0, p1;
+              unpack2(fma2(pack2(s[k + 2 * e], s[k + 2 * e + 1]), mul2, base2), &p0, &p1);
+              p0 = ex2(p0), p1 = ex2(p1);
+              sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(p1), "f"(p0));
             }
-            tmem_st16(s_at + k / 2, w);
+            tmem_st16(s_at + (part * kCols + k) / 2, w);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float s0, s1;
+          unpack2(add2(sum[0], sum[1]), &s0, &s1);
+          l += s0 + s1;
           tmem_wait_st();
+        } else if constexpr (kSplit == 2) {
+          named_bar_sync(1 + st, 256);
         }
         tmem_fence_before();
         mbar_arrive(pbar);
@@ -659,21 +735,24 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
 
       if (live) {
         // ------------------------------------------------------ epilogue
+        if constexpr (kSplit == 2) l += exchange(l, turn);
         mbar_wait(obar, turn ^ 1, timed_out);
         __syncwarp();
         tmem_fence_after();
         if (work) {
           const bool valid = st * kTile + row < g.rows;
           const bool odd = *reinterpret_cast<volatile int32_t*>(&bars->odd) != 0;
-          const int head = g.h * a.group + (g.m * MR + st * kTile + row) % a.group;
-          const int64_t orow = g.row0 + token;
+          const int i = g.m * MR + st * kTile + row;
+          const int head = g.h * a.group + i % a.group;
+          const int64_t orow = g.row0 + i / a.group;
           const int slot = 2 * blockIdx.x + (g.begins ? 1 : 0);
           const float inv = g.whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
           const int prow = st * kTile + row;
 #pragma unroll 1
-          for (int k = 0; k < DP; k += 32) {
-            uint32_t x[32];
-            tmem_ld32(o_at + k, x);
+          for (int k0 = 0; k0 < kOut; k0 += 16) {
+            const int k = part * kOut + k0;
+            uint32_t x[16];
+            tmem_ld16(o_at + k0, x);
             tmem_wait_ld();
             float* o = reinterpret_cast<float*>(x);
             __syncwarp();
@@ -689,7 +768,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
                 const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
                     a.v + id * a.block + (t % a.page) * a.token + g.h * a.head) + k;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < 16; ++e)
                   if (k + e < a.dim && !(fabsf(__bfloat162float(v[e])) < kInf))
                     o[e] += __bfloat162float(v[e]);
               }
@@ -697,7 +776,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
             if (g.whole) {
               char* out = a.out + orow * a.o_row + head * a.o_head + k * 2;
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
+              for (int e = 0; e < 16; e += 8) {
                 uint4 w;
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(o[e + 1] * inv), "f"(o[e] * inv));
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(o[e + 3] * inv), "f"(o[e + 2] * inv));
@@ -707,12 +786,12 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
+              for (int e = 0; e < 16; e += 4)
                 p.o[(static_cast<int64_t>(slot) * (DP / 4) + (k + e) / 4) * MR + prow] =
                     make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
-          if (valid) {
+          if (valid && part == 0) {
             const float mc = m == -kInf ? -kInf : m * c;
             if (!g.whole)
               p.ml[static_cast<int64_t>(slot) * MR + prow] = make_float2(mc, l);
@@ -722,8 +801,6 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           tmem_fence_before();
         }
       }
-      g = next;
-      more = has_next;
     }
   }
   if (timed_out && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_TIMEOUT);
