@@ -154,14 +154,14 @@ namespace {
 
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr size_t kRecordBytes = round256(sizeof(AttnRecord) * kMaxWorkers);
-constexpr size_t kMlBytes = sizeof(float2) * 2 * kMaxWorkers * kTile;
+constexpr size_t kMlBytes = sizeof(float2) * 2 * kMaxWorkers * kRows;
 
 bool on_tensor_cores(int dtype, int head_dim) { return dtype == SV_BF16 && head_dim <= 128; }
 
 size_t workspace_bytes_of(int dtype, int head_dim) {
   if (!on_tensor_cores(dtype, head_dim)) return 256;
   const size_t dp = head_dim <= 64 ? 64 : 128;
-  return kRecordBytes + kMlBytes + sizeof(float) * 2 * kMaxWorkers * kTile * dp;
+  return kRecordBytes + kMlBytes + sizeof(float) * 2 * kMaxWorkers * kRows * dp;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -208,7 +208,7 @@ int launch_mma(const MmaArgs& p, int grid, const CUtensorMap& km, const CUtensor
                ? launch(attn_mma_kernel<NS, DP, true>, dim3(grid), threads, smem, 1, false, st, p, km, vm)
                : launch(attn_mma_kernel<NS, DP, false>, dim3(grid), threads, smem, 1, false, st, p, km, vm);
   if (rc != SV_OK || grid == 1) return rc;  // one worker cuts no item
-  return launch(attn_combine_kernel<NS * kTile, DP>, dim3(grid, NS * kTile / kCombineRows),
+  return launch(attn_combine_kernel<NS * kRows, DP>, dim3(grid, NS * kRows / kCombineRows),
                 kCombineThreads, 0, 1, true, st, p);
 }
 
@@ -234,9 +234,9 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
                     !encode_cache(&vm, a.v, a, kv_heads, p.box)))
     return SV_ERR_CUDA;
   const int64_t rows = std::min<int64_t>(a.max_len, a.n_rows) * a.group;
-  const int ns = rows > kTile ? 2 : 1;
+  const int ns = rows > kRows ? 2 : 1;
   const int64_t keys = static_cast<int64_t>(a.table_width) * a.page;
-  const int64_t tiles = (rows + ns * kTile - 1) / (ns * kTile) * ((keys + kTile - 1) / kTile) *
+  const int64_t tiles = (rows + ns * kRows - 1) / (ns * kRows) * ((keys + kTile - 1) / kTile) *
                         a.B * kv_heads;
   const int64_t most = ns == 1 ? std::min(2 * d.sms, kMaxWorkers) : std::min(d.sms, kMaxWorkers / 2);
   const int grid = static_cast<int>(std::min(most, tiles));

@@ -3,30 +3,30 @@
 // The query rows of a request that share a key/value head -- l tokens times the
 // group of G heads -- are packed into tiles of 128 rows, row i = token i / G,
 // head i % G of the group, so a key/value tile is read once for all of them.
-// An item is (request, kv head, NS row tiles); its work is the 128-key tiles
+// An item is (request, kv head, NS row tiles); its work is the 64-key tiles
 // from the first key that its first row sees to the last that its last row
 // sees.  All items' tiles in a row are cut into equal runs, one a worker (CTA);
 // a worker whose run starts or ends inside an item leaves an unnormalised
 // partial (O, m, l) in the workspace, and the combine kernel joins them.
 //
-// Per stream of 128 rows and key tile:
-//   S = Q K^T   tcgen05.mma from shared memory into 128 tensor memory columns
+// Per stream of 128 rows (one softmax warpgroup, a thread a row) and key tile:
+//   S = Q K^T   tcgen05.mma from shared memory into 64 tensor memory columns
 //   P = 2^(S c - m c), c = scale log2 e, rounded to bf16 over S's own columns
 //   O += P V    tcgen05.mma with P from tensor memory
-// The running maximum m of a row rises lazily: P may grow to 2^8 before O is
-// rescaled, so most tiles leave O alone; the row sum l is of the unrounded P, in
-// fp32.  P keeps 8 bits of mantissa: an error of at most 2^-9 a weight, of the
-// size of the output's own rounding, for tensor products at full rate.
+// S has two buffers, and Q K^T runs two tiles ahead of P V, so that neither the
+// softmax nor the tensor core waits for the other's latency.  (128-key tiles
+// with one buffer: 3,400 cycles from S to P beside 1,024 of products a stream
+// and tile, 1.58 ms for the 4,096-token chunks; two warpgroups a stream to halve
+// the softmax: 1.77 ms.)  The running maximum m of a row rises lazily: P may grow
+// to 2^8 before O is rescaled, so most tiles leave O alone; the row sum l is of
+// the unrounded P, in fp32.  P keeps 8 significant bits: an error of at most 2^-8
+// a weight, of the size of the output's own rounding, for tensor products at
+// full rate.
 //
 // NS = 1 (at most 128 rows an item, decoding and verify steps: the cache's
-// bytes bound it): two CTAs an SM, each with one stream and a ring of 64-key
-// copies; while one's softmax runs, the other's products do.
-// One softmax warpgroup, a thread a row.
+// bytes bound it): two CTAs an SM, each with one stream.
 // NS = 2 (longer chunks: the products bound it): one CTA an SM, two streams
-// over the same key/value tiles, the tensor core alternating between them: its
-// 1,024 cycles a tile for one stream are the time that the other's softmax may
-// take.  Two warpgroups a stream, a thread half a row's columns: with one, the
-// softmax took 3,400 cycles from S to P.
+// over the same key/value tiles, the tensor core alternating between them.
 //
 // Keys and values come by tensor copies of whole page pieces (page sizes that
 // are a multiple of 64 or 8, 16, 32) and by 16-byte copies of single rows
@@ -48,7 +48,8 @@
 namespace sv {
 namespace serve {
 
-constexpr int kTile = 128;        // keys of a tile
+constexpr int kRows = 128;        // query rows of a stream
+constexpr int kTile = 64;         // keys of a tile
 constexpr int kMaxWorkers = 320;  // partials are laid out for this many
 constexpr float kRescale = 8.0f;  // log2 of how far P may exceed 1 before O is rescaled
 
@@ -66,15 +67,12 @@ struct MmaArgs {
   float4* o;              // [2 * kMaxWorkers][DP / 4][rows]
 };
 
-__host__ __device__ constexpr int attn_unit_tokens(int ns) { return ns == 1 ? 64 : 128; }
-__host__ __device__ constexpr int attn_units(int ns, int dp) { return (ns == 1 ? 5 : 4) * 128 / dp; }
-__host__ __device__ constexpr int attn_softmax_warps(int ns) { return ns == 1 ? 4 : 16; }
-__host__ __device__ constexpr int attn_threads(int ns) { return (attn_softmax_warps(ns) + 4) * 32; }
-// query tiles, ring, barriers, the softmax warps' walks, and for two warpgroups
-// a stream what they exchange
+constexpr int kMaxUnits = 10;
+__host__ __device__ constexpr int attn_units(int ns, int dp) { return ns == 1 && dp == 128 ? 5 : kMaxUnits; }
+__host__ __device__ constexpr int attn_threads(int ns) { return (ns * 4 + 2) * 32; }
+// query tiles, ring of key and value tiles, barriers, the softmax warps' walks
 __host__ __device__ constexpr int attn_smem(int ns, int dp) {
-  return ns * kTile * dp * 2 + attn_units(ns, dp) * attn_unit_tokens(ns) * dp * 2 + 256 +
-         attn_softmax_warps(ns) * 104 + (ns == 1 ? 0 : ns * 4 * kTile * 4);
+  return ns * kRows * dp * 2 + attn_units(ns, dp) * kTile * dp * 2 + 320 + ns * 4 * 104;
 }
 
 // ---------------------------------------------------------------- work
@@ -229,30 +227,23 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem* sm, Walk<MR>* w
 // ---------------------------------------------------------------- kernel
 template <int NS, int DP>
 struct AttnSmem {
-  static constexpr int kUnitTokens = attn_unit_tokens(NS);
   static constexpr int kUnits = attn_units(NS, DP);
-  static constexpr int kUnitBytes = kUnitTokens * DP * 2;
-  static constexpr int kQBytes = kTile * DP * 2;
+  static constexpr int kUnitBytes = kTile * DP * 2;
+  static constexpr int kQBytes = kRows * DP * 2;
   static constexpr int kChunks = DP / 64;
-  static constexpr int kPerTile = kTile / kUnitTokens;  // units of a K or V tile
 };
 
 struct AttnBars {
-  uint64_t full[10], empty[10];
-  uint64_t q[2], s[2], p[2], o[2], idle;
+  uint64_t full[kMaxUnits], empty[kMaxUnits];
+  uint64_t q[2], s[2][2], p[2][2], o[2][2], idle;  // by stream; s, p and o by S buffer too
   uint32_t tmem;
   int32_t odd;  // a non-finite value was set aside in this CTA
 };
-static_assert(sizeof(AttnBars) <= 256, "barrier block");
+static_assert(sizeof(AttnBars) <= 320, "barrier block");
 
-// Registers: the softmax warps hold their part of a tile's row, the others
-// little.  Of the launch's share (NS = 1: 256 threads x 128, NS = 2: 640 x 96)
-// the copying and issuing warpgroup gives up what the softmax warpgroups take:
-// 128 x 40 + 128 x 216 = 256 x 128, and 128 x 64 + 512 x 104 = 640 x 96.
-template <int NS>
-struct AttnRegs {
-  static constexpr int kLess = NS == 1 ? 40 : 64, kMore = NS == 1 ? 216 : 104;
-};
+// The ring's order in a segment of n tiles is that of the products: K 0, K 1,
+// V 0, K 2, V 1, K 3, ..  Position of the V of tile i:
+__device__ __forceinline__ int v_position(int n, int i) { return min(n, i + 2) + i; }
 
 // Two floats at once: a * b + c and a + b.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -285,22 +276,20 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
     const MmaArgs p, const __grid_constant__ CUtensorMap kmap,
     const __grid_constant__ CUtensorMap vmap) {
   using L = AttnSmem<NS, DP>;
-  constexpr int MR = NS * kTile;
+  constexpr int MR = NS * kRows;
   constexpr int kThreads = attn_threads(NS);
   constexpr uint32_t kCols = NS == 1 ? 256 : 512;
-  // tensor memory columns: S (and P) of each stream, then O of each
-  constexpr uint32_t kO = NS * kTile;
+  // tensor memory columns: two S buffers of each stream, then O of each
+  constexpr uint32_t kO = NS * 2 * kTile;
   extern __shared__ __align__(1024) char smem[];
   const AttnArgs& a = p.a;
   char* const qbuf = smem;
   char* const ring = smem + NS * L::kQBytes;
   AttnBars* const bars = reinterpret_cast<AttnBars*>(ring + L::kUnits * L::kUnitBytes);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kSoftmax = attn_softmax_warps(NS), kLoadWarp = kSoftmax, kMmaWarp = kSoftmax + 1;
-  constexpr int kSplit = kSoftmax / (NS * 4);  // warpgroups a stream
-  WarpWalk<MR>* const walks = reinterpret_cast<WarpWalk<MR>*>(reinterpret_cast<char*>(bars) + 256);
+  WarpWalk<MR>* const walks = reinterpret_cast<WarpWalk<MR>*>(reinterpret_cast<char*>(bars) + 320);
   static_assert(sizeof(WarpWalk<MR>) <= 104, "walk block");
-  float* const swap = reinterpret_cast<float*>(reinterpret_cast<char*>(walks) + kSoftmax * 104);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kSoftmax = NS * 4, kLoadWarp = kSoftmax, kMmaWarp = kSoftmax + 1;
   bool timed_out = false;
 
   Walk<MR> walk;
@@ -314,10 +303,12 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       mbar_init(smem_addr(&bars->empty[i]), 1);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_addr(&bars->q[s]), 128 * kSplit);
-      mbar_init(smem_addr(&bars->s[s]), 1);
-      mbar_init(smem_addr(&bars->p[s]), 128 * kSplit);
-      mbar_init(smem_addr(&bars->o[s]), 1);
+      mbar_init(smem_addr(&bars->q[s]), 128);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_addr(&bars->s[s][b]), 1);
+        mbar_init(smem_addr(&bars->p[s][b]), 128);
+        mbar_init(smem_addr(&bars->o[s][b]), 1);
+      }
     }
     mbar_init(smem_addr(&bars->idle), 1);
     bars->odd = 0;
@@ -332,8 +323,6 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   auto full = [&](int u) { return smem_addr(&bars->full[u]); };
   auto empty = [&](int u) { return smem_addr(&bars->empty[u]); };
 
-  if (warp >= kSoftmax) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AttnRegs<NS>::kLess));
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------- copies
     int u = 0;          // ring position
@@ -343,67 +332,68 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
     Segment g;
     while (walk.next(p, &g)) {
       const int32_t* table = a.table + g.r * a.table_stride;
-      for (int tile = g.tile0; tile < g.tile1; ++tile) {
-        for (int half = 0; half < 2 * L::kPerTile; ++half) {
-          const bool val = half >= L::kPerTile;
-          const int t0 = tile * kTile + (half % L::kPerTile) * L::kUnitTokens;
-          const uint32_t dst = ring_addr + u * L::kUnitBytes;
-          if constexpr (TMA) {
-            // lane: box lane / chunks of the unit, column chunk lane % chunks
-            const int boxes = L::kUnitTokens / p.box;
-            const int t = t0 + lane / L::kChunks * p.box, c = lane % L::kChunks;
-            const bool on = lane < boxes * L::kChunks && t < g.kv_end;
-            int id = 0;
-            if (on) {
-              id = __ldg(table + t / a.page);
+      const int n = g.tile1 - g.tile0;
+      int ki = 0, vi = 0;
+      for (int x = 0; x < 2 * n; ++x) {
+        // K 0, K 1, then V and K in turn until the Ks are through
+        const bool val = ki == n || (ki >= 2 && ki == vi + 2);
+        const int t0 = (g.tile0 + (val ? vi++ : ki++)) * kTile;
+        const uint32_t dst = ring_addr + u * L::kUnitBytes;
+        if constexpr (TMA) {
+          // lane: box lane / chunks of the unit, column chunk lane % chunks
+          const int boxes = kTile / p.box;
+          const int t = t0 + lane / L::kChunks * p.box, c = lane % L::kChunks;
+          const bool on = lane < boxes * L::kChunks && t < g.kv_end;
+          int id = 0;
+          if (on) {
+            id = __ldg(table + t / a.page);
+            if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
+          }
+          const unsigned live = __ballot_sync(~0u, on);
+          if (issued >= L::kUnits) mbar_wait(empty(u), turn ^ 1, timed_out);
+          if (lane == 0)
+            mbar_arrive_expect_tx(full(u), static_cast<uint32_t>(__popc(live)) * p.box * 128);
+          __syncwarp();
+          if (on)
+            tma_load4(dst + c * (kTile * 128) + (t - t0) * 128, val ? &vmap : &kmap, c * 64,
+                      t % a.page, g.h, id, full(u));
+        } else {
+          // lane: the addresses of rows lane and lane + 32; 16-byte pieces
+          constexpr int kPieces = DP / 8;
+          const char* at[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = t0 + k * 32 + lane;
+            at[k] = nullptr;
+            if (t < g.kv_end) {
+              int id = __ldg(table + t / a.page);
               if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
-            }
-            const unsigned live = __ballot_sync(~0u, on);
-            if (issued >= L::kUnits) mbar_wait(empty(u), turn ^ 1, timed_out);
-            if (lane == 0)
-              mbar_arrive_expect_tx(full(u), static_cast<uint32_t>(__popc(live)) * p.box * 128);
-            __syncwarp();
-            if (on)
-              tma_load4(dst + c * (L::kUnitTokens * 128) + (t - t0) * 128, val ? &vmap : &kmap,
-                        c * 64, t % a.page, g.h, id, full(u));
-          } else {
-            // lane: the addresses of rows lane, lane + 32, ..; 16-byte pieces
-            constexpr int kRows = L::kUnitTokens / 32, kPieces = DP / 8;
-            const char* at[kRows];
-#pragma unroll
-            for (int k = 0; k < kRows; ++k) {
-              const int t = t0 + k * 32 + lane;
-              at[k] = nullptr;
-              if (t < g.kv_end) {
-                int id = __ldg(table + t / a.page);
-                if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
-                at[k] = (val ? a.v : a.k) + id * a.block + (t % a.page) * a.token + g.h * a.head;
-              }
-            }
-            if (issued >= L::kUnits) mbar_wait(empty(u), turn ^ 1, timed_out);
-#pragma unroll
-            for (int k = 0; k < kRows; ++k)
-              for (int i = 0; i < kPieces; ++i) {
-                const int row = i * 32 / kPieces + lane / kPieces, j = lane % kPieces;
-                const char* src = reinterpret_cast<const char*>(
-                    __shfl_sync(~0u, reinterpret_cast<unsigned long long>(at[k]), row));
-                const int rr = k * 32 + row;
-                const bool on = src != nullptr && j * 8 < a.dim;
-                cp_async16(dst + (j / 8) * (L::kUnitTokens * 128) + rr * 128 +
-                               (((j & 7) ^ (rr & 7)) << 4),
-                           on ? src + j * 16 : a.k, on ? 16 : 0);
-              }
-            cp_async_commit();
-            // the unit before the last has landed: hand it over
-            if (issued >= 2) {
-              cp_async_wait<2>();
-              fence_async_smem();
-              mbar_arrive(full((u + L::kUnits - 2) % L::kUnits));
+              at[k] = (val ? a.v : a.k) + id * a.block + (t % a.page) * a.token + g.h * a.head;
             }
           }
-          ++issued;
-          if (++u == L::kUnits) u = 0, turn ^= 1;
+          if (issued >= L::kUnits) mbar_wait(empty(u), turn ^ 1, timed_out);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            for (int i = 0; i < kPieces; ++i) {
+              const int row = i * 32 / kPieces + lane / kPieces, j = lane % kPieces;
+              const char* src = reinterpret_cast<const char*>(
+                  __shfl_sync(~0u, reinterpret_cast<unsigned long long>(at[k]), row));
+              const int rr = k * 32 + row;
+              const bool on = src != nullptr && j * 8 < a.dim;
+              cp_async16(dst + (j / 8) * (kTile * 128) + rr * 128 + (((j & 7) ^ (rr & 7)) << 4),
+                         on ? src + j * 16 : a.k, on ? 16 : 0);
+            }
+          cp_async_commit();
+          // the unit before the last has landed: hand it over
+          if (issued >= 2) {
+            cp_async_wait<2>();
+            fence_async_smem();
+            mbar_arrive(full((u + L::kUnits - 2) % L::kUnits));
+          }
         }
+        ++issued;
+        if (++u == L::kUnits) u = 0, turn ^= 1;
       }
     }
     if constexpr (!TMA) {
@@ -415,7 +405,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       cp_async_wait<0>();
       fence_async_smem();
       mbar_arrive(full((u + L::kUnits - 1) % L::kUnits));
-    } else if (timed_out) {  // no copy outlives the CTA (units issued late wait for their own)
+    } else if (timed_out) {  // no copy outlives the CTA
       for (int i = 0; i < L::kUnits; ++i) {
         bool late = false;
         mbar_wait(full(i), turn ^ (i < u ? 0u : 1u), late);
@@ -425,131 +415,97 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- products
     if (lane == 0) {
-      constexpr uint32_t kQk = mma_idesc(L::kUnitTokens, false), kPv = mma_idesc(DP, true);
+      constexpr uint32_t kQk = mma_idesc(kTile, false), kPv = mma_idesc(DP, true);
       int u = 0;
-      uint32_t turn = 0;          // parity of the ring's turn
-      uint32_t pturn[2] = {0, 0};  // parity of each stream's next P
+      uint32_t turn = 0;                // parity of the ring's turn
+      uint32_t tiles[2] = {0, 0};       // each stream's S tiles so far
+      uint32_t done[2] = {0, 0};        // and P tiles
       uint32_t qturn = 0;
-      auto wait_unit = [&](int unit, uint32_t par) {
-        mbar_wait(full(unit), par, timed_out);
-        tmem_fence_after();
+      auto step = [&]() {
+        if (++u == L::kUnits) u = 0, turn ^= 1;
       };
-      // S columns [n0, n0 + unit) of stream s from the unit at `kb`
-      auto qk = [&](int s, uint32_t kb, int n0) {
+      // S of the streams [0, ns) from the K unit at u
+      auto qk = [&](int s, int unit) {
+        const uint32_t kb = ring_addr + unit * L::kUnitBytes, b = tiles[s] & 1;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint32_t at = (k % 4) * 32;
-          mma_ss(tmem + s * kTile + n0,
-                 smem_desc(q_addr + s * L::kQBytes + k / 4 * (kTile * 128) + at, 0),
-                 smem_desc(kb + k / 4 * (L::kUnitTokens * 128) + at, 0), kQk, k > 0);
+          mma_ss(tmem + (s * 2 + b) * kTile,
+                 smem_desc(q_addr + s * L::kQBytes + k / 4 * (kRows * 128) + at, 0),
+                 smem_desc(kb + k / 4 * (kTile * 128) + at, 0), kQk, k > 0);
         }
-      };
-      auto pv = [&](int s, uint32_t vb, int k0, bool add) {
-#pragma unroll
-        for (int k = 0; k < L::kUnitTokens / 16; ++k)
-          mma_ts(tmem + kO + s * DP, tmem + s * kTile + (k0 + k * 16) / 2,
-                 smem_desc(vb + k * 2048, DP > 64 ? L::kUnitTokens * 128 : 0), kPv, add || k > 0);
+        ++tiles[s];
+        return smem_addr(&bars->s[s][b]);
       };
       Segment g;
-      if constexpr (NS == 1) {
-        while (walk.next(p, &g)) {
-          mbar_wait(smem_addr(&bars->q[0]), qturn, timed_out);
-          qturn ^= 1;
-          for (int tile = g.tile0; tile < g.tile1; ++tile) {
-#pragma unroll
-            for (int i = 0; i < L::kPerTile; ++i) {
-              wait_unit(u, turn);
-              qk(0, ring_addr + u * L::kUnitBytes, i * L::kUnitTokens);
-              mma_commit(empty(u));
-              if (++u == L::kUnits) u = 0, turn ^= 1;
-            }
-            mma_commit(smem_addr(&bars->s[0]));
-            mbar_wait(smem_addr(&bars->p[0]), pturn[0], timed_out);
-            pturn[0] ^= 1;
-            tmem_fence_after();
-#pragma unroll
-            for (int i = 0; i < L::kPerTile; ++i) {
-              wait_unit(u, turn);
-              pv(0, ring_addr + u * L::kUnitBytes, i * L::kUnitTokens, tile > g.tile0 || i > 0);
-              mma_commit(empty(u));
-              if (++u == L::kUnits) u = 0, turn ^= 1;
-            }
-            mma_commit(smem_addr(&bars->o[0]));
-          }
-        }
-      } else {
-        auto step = [&]() {
-          if (++u == L::kUnits) u = 0, turn ^= 1;
-        };
-        while (walk.next(p, &g)) {
-          const int ns = g.rows > kTile ? 2 : 1;
-          for (int s = 0; s < 2; ++s) mbar_wait(smem_addr(&bars->q[s]), qturn, timed_out);
-          qturn ^= 1;
-          if (ns == 1) mbar_arrive(smem_addr(&bars->idle));  // the second stream may go on
-          wait_unit(u, turn);
+      while (walk.next(p, &g)) {
+        const int ns = NS == 2 && g.rows > kRows ? 2 : 1, n = g.tile1 - g.tile0;
+        for (int s = 0; s < NS; ++s) mbar_wait(smem_addr(&bars->q[s]), qturn, timed_out);
+        qturn ^= 1;
+        if (ns < NS) mbar_arrive(smem_addr(&bars->idle));  // the second stream may go on
+        for (int i = 0; i < min(2, n); ++i) {
+          mbar_wait(full(u), turn, timed_out);
+          tmem_fence_after();
           for (int s = 0; s < ns; ++s) {
-            qk(s, ring_addr + u * L::kUnitBytes, 0);
+            const uint32_t ready = qk(s, u);
             if (s == ns - 1) mma_commit(empty(u));
-            mma_commit(smem_addr(&bars->s[s]));
+            mma_commit(ready);
           }
           step();
-          for (int tile = g.tile0; tile < g.tile1; ++tile) {
-            const int vu = u;
-            const uint32_t vt = turn;
-            step();
-            for (int s = 0; s < ns; ++s) {
-              mbar_wait(smem_addr(&bars->p[s]), pturn[s], timed_out);
-              pturn[s] ^= 1;
-              tmem_fence_after();
-              if (s == 0) wait_unit(vu, vt);
-              pv(s, ring_addr + vu * L::kUnitBytes, 0, tile > g.tile0);
-              if (s == ns - 1) mma_commit(empty(vu));
-              mma_commit(smem_addr(&bars->o[s]));
-              if (tile + 1 < g.tile1) {
-                if (s == 0) wait_unit(u, turn);
-                qk(s, ring_addr + u * L::kUnitBytes, 0);
-                if (s == ns - 1) mma_commit(empty(u));
-                mma_commit(smem_addr(&bars->s[s]));
+        }
+        for (int i = 0; i < n; ++i) {
+          const int vu = u;
+          const uint32_t vt = turn;
+          step();
+          const bool ahead = i + 2 < n;
+          for (int s = 0; s < ns; ++s) {
+            const uint32_t b = done[s] & 1;
+            mbar_wait(smem_addr(&bars->p[s][b]), done[s] >> 1 & 1, timed_out);
+            ++done[s];
+            if (s == 0) mbar_wait(full(vu), vt, timed_out);
+            tmem_fence_after();
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ts(tmem + kO + s * DP, tmem + (s * 2 + b) * kTile + k * 8,
+                     smem_desc(ring_addr + vu * L::kUnitBytes + k * 2048, DP > 64 ? kTile * 128 : 0),
+                     kPv, i > 0 || k > 0);
+            if (s == ns - 1) mma_commit(empty(vu));
+            mma_commit(smem_addr(&bars->o[s][b]));
+            if (ahead) {
+              if (s == 0) {
+                mbar_wait(full(u), turn, timed_out);
+                tmem_fence_after();
               }
+              const uint32_t ready = qk(s, u);
+              if (s == ns - 1) mma_commit(empty(u));
+              mma_commit(ready);
             }
-            if (tile + 1 < g.tile1) step();
           }
+          if (ahead) step();
         }
       }
     }
     __syncwarp();
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AttnRegs<NS>::kMore));
     // ---------------------------------------------------------- softmax
-    constexpr int kCols = kTile / kSplit;   // columns of S a thread
-    constexpr int kOut = DP / kSplit;       // columns of O a thread
-    const int st = warp / (4 * kSplit);     // stream
-    const int part = (warp >> 2) % kSplit;  // columns [part * kCols, ..)
-    const int row = tid & 127;              // row of the stream's tile
-    const int wrow = (warp & 3) * 32;       // the warp's first row
+    const int st = warp >> 2;          // stream
+    const int row = tid & 127;         // row of the stream's tile
+    const int wrow = (warp & 3) * 32;  // the warp's first row
     const uint32_t lanes = static_cast<uint32_t>(wrow) << 16;
-    const uint32_t s_at = tmem + lanes + st * kTile,
-                   o_at = tmem + lanes + kO + st * DP + part * kOut;
-    const uint32_t sbar = smem_addr(&bars->s[st]), pbar = smem_addr(&bars->p[st]),
-                   obar = smem_addr(&bars->o[st]);
+    const uint32_t s_at = tmem + lanes + st * 2 * kTile, o_at = tmem + lanes + kO + st * DP;
+    // the stream's O up to tile t: S of tile t + 1 tells of tile t - 1, so at most
+    // the last phase of this barrier can be open
+    auto wait_o = [&](uint32_t t) {
+      mbar_wait(smem_addr(&bars->o[st][t & 1]), t >> 1 & 1, timed_out);
+      __syncwarp();
+      tmem_fence_after();
+    };
     const float c = fabsf(a.scale2);
     WarpWalk<MR>* const ww = walks + warp;
-    uint32_t turn = 0;  // parity of the stream's next tile
-    uint32_t idle = 0;  // parity of the next segment without rows here
-    int vu = 0;         // ring position of the tile's first V unit
-    uint32_t vturn = 0;
-    auto ring_step = [&](int n) {
-      vu += n;
-      if (vu >= L::kUnits) vu -= L::kUnits, vturn ^= 1;
-    };
-    // x of this thread's row in the stream's other warpgroup; `slot` in turn
-    auto exchange = [&](float x, int slot) {
-      float* at = swap + (st * 2 + slot) * 2 * kTile + row;
-      at[part * kTile] = x;
-      named_bar_sync(1 + st, 256);
-      return at[(part ^ 1) * kTile];
-    };
+    uint32_t tiles = 0;  // the stream's tiles so far
+    uint32_t idle = 0;   // parity of the next segment without rows here
+    int u0 = 0;          // ring position of the segment's first unit, and its turn
+    uint32_t turn0 = 0;
     // the walk's next segment, by lane 0, into shared memory (tile1 = -1: none)
     auto advance = [&]() {
       __syncwarp();
@@ -565,20 +521,20 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
     // the next segment's query rows: lane's own row address, then 16-byte pieces
     auto load_q = [&]() {
       const Segment& n = ww->next;
-      const int i = n.m * MR + st * kTile + wrow + lane;
+      const int i = n.m * MR + st * kRows + wrow + lane;
       const char* src = nullptr;
-      if (st * kTile + wrow + lane < n.rows)
+      if (st * kRows + wrow + lane < n.rows)
         src = a.q + static_cast<int64_t>(n.row0 + i / a.group) * a.q_row +
               static_cast<int64_t>(n.h * a.group + i % a.group) * a.q_head;
       constexpr int kPieces = DP / 8;
-      if (st * kTile + wrow < n.rows) {
+      if (st * kRows + wrow < n.rows) {
 #pragma unroll 4
-        for (int k = part; k < kPieces; k += kSplit) {
+        for (int k = 0; k < kPieces; ++k) {
           const int rr = k * 32 / kPieces + lane / kPieces, j = lane % kPieces;
           const char* from = reinterpret_cast<const char*>(
               __shfl_sync(~0u, reinterpret_cast<unsigned long long>(src), rr));
           const bool ok = from != nullptr && j * 8 < a.dim;
-          cp_async16(q_addr + st * L::kQBytes + (j / 8) * (kTile * 128) + (wrow + rr) * 128 +
+          cp_async16(q_addr + st * L::kQBytes + (j / 8) * (kRows * 128) + (wrow + rr) * 128 +
                          (((j & 7) ^ (rr & 7)) << 4),
                      ok ? from + j * 16 : a.q, ok ? 16 : 0);
         }
@@ -587,7 +543,6 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
     };
 
     if (lane == 0) ww->walk = walk;
-    __syncwarp();
     advance();
     load_q();
     while (ww->next.tile1 >= 0) {
@@ -595,9 +550,9 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       cp_async_wait<0>();
       fence_async_smem();
       mbar_arrive(smem_addr(&bars->q[st]));
-      const bool live = st * kTile < g.rows;         // the stream has rows
-      const bool work = st * kTile + wrow < g.rows;  // the warp has rows
-      const int pos = g.seq - g.l + (g.m * MR + st * kTile + row) / a.group;  // of this row
+      const bool live = st * kRows < g.rows;         // the stream has rows
+      const bool work = st * kRows + wrow < g.rows;  // the warp has rows
+      const int pos = g.seq - g.l + (g.m * MR + st * kRows + row) / a.group;  // of this row
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       // keys that every row of the item sees: [all_lo, all_hi)
       const int all_hi = g.seq - g.l + g.m * MR / a.group + 1;
@@ -605,88 +560,80 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           ? max(0, g.seq - g.l + (g.m * MR + g.rows - 1) / a.group - a.window + 1) : 0;
       float m = -kInf, l = 0.0f;
 
-      if (!live) {  // the other stream's tiles pass through the ring
+      if (!live) {
         mbar_wait(smem_addr(&bars->idle), idle, timed_out);
         __syncwarp();
         idle ^= 1;
-        for (int tile = g.tile0; tile < g.tile1; ++tile) ring_step(2 * L::kPerTile);
         advance();
         if (ww->next.tile1 >= 0) load_q();
       }
-      for (int tile = g.tile0; live && tile < g.tile1; ++tile) {
+      for (int tile = g.tile0; live && tile < g.tile1; ++tile, ++tiles) {
         const int t0 = tile * kTile;
-        ring_step(L::kPerTile);  // past K: at V
+        const uint32_t buf = tiles & 1;
         const bool edge = t0 + kTile > all_hi || t0 < all_lo;
-        if (edge) {  // set aside non-finite values that not all rows see
-          int un = vu;
-          uint32_t ut = vturn;
-#pragma unroll
-          for (int i = 0; i < L::kPerTile; ++i) {
-            mbar_wait(full(un), ut, timed_out);
-            char* unit = ring + un * L::kUnitBytes;
-            for (int at = row + part * 128; at < L::kUnitBytes / 16; at += 128 * kSplit) {
-              const int t = t0 + i * L::kUnitTokens + (at >> 3) % L::kUnitTokens;
-              if (t >= all_lo && t < all_hi) continue;
-              uint4 v = *reinterpret_cast<const uint4*>(unit + at * 16);
-              uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-              bool odd = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, odd = true;
-                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, odd = true;
-              }
-              if (odd) {
-                if (t < g.seq) bars->odd = 1;
-                __threadfence_block();
-                *reinterpret_cast<uint4*>(unit + at * 16) = v;
-              }
-            }
-            if (++un == L::kUnits) un = 0, ut ^= 1;
-          }
-          fence_async_smem();
-        }
-        mbar_wait(sbar, turn, timed_out);
+        mbar_wait(smem_addr(&bars->s[st][buf]), tiles >> 1 & 1, timed_out);
         __syncwarp();
         tmem_fence_after();
         if (tile + 1 == g.tile1) {  // the last S is formed: the query buffer is free
           advance();
           if (ww->next.tile1 >= 0) load_q();
         }
-        if (work) {
-          uint32_t x[kCols];
+        if (edge) {  // set aside non-finite values that not all rows see; S is there,
+                     // so the V unit's last occupant is gone and its turn is this one
+          const int at_v = u0 + v_position(g.tile1 - g.tile0, tile - g.tile0);
+          mbar_wait(full(at_v % L::kUnits), (turn0 ^ (at_v / L::kUnits)) & 1, timed_out);
+          char* unit = ring + at_v % L::kUnits * L::kUnitBytes;
+          for (int at = row; at < L::kUnitBytes / 16; at += 128) {
+            const int t = t0 + (at >> 3) % kTile;
+            if (t >= all_lo && t < all_hi) continue;
+            uint4 v = *reinterpret_cast<const uint4*>(unit + at * 16);
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+            bool odd = false;
 #pragma unroll
-          for (int k = 0; k < kCols; k += 32) tmem_ld32(s_at + part * kCols + k, x + k);
+            for (int e = 0; e < 4; ++e) {
+              if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, odd = true;
+              if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, odd = true;
+            }
+            if (odd) {
+              if (t < g.seq) bars->odd = 1;
+              __threadfence_block();
+              *reinterpret_cast<uint4*>(unit + at * 16) = v;
+            }
+          }
+          fence_async_smem();
+        }
+        if (work) {
+          uint32_t x[kTile];
+          tmem_ld32(s_at + buf * kTile, x);
+          tmem_ld32(s_at + buf * kTile + 32, x + 32);
           tmem_wait_ld();
           float* s = reinterpret_cast<float*>(x);
           if (a.scale2 < 0.0f) {
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) s[k] = -s[k];
+            for (int k = 0; k < kTile; ++k) s[k] = -s[k];
           }
           if (edge) {
-            const int from = lo - t0 - part * kCols, to = pos + 1 - t0 - part * kCols;
+            const int from = lo - t0, to = pos + 1 - t0;
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) s[k] = k >= from && k < to ? s[k] : -kInf;
+            for (int k = 0; k < kTile; ++k) s[k] = k >= from && k < to ? s[k] : -kInf;
           }
           float mx[4] = {m, s[0], s[1], s[2]};
           mx[3] = fmaxf(mx[3], s[3]);
 #pragma unroll
-          for (int k = 4; k < kCols; k += 8)
+          for (int k = 4; k < kTile; k += 8)
 #pragma unroll
-            for (int e = 0; e < 4 && k + 2 * e < kCols; ++e)
+            for (int e = 0; e < 4 && k + 2 * e < kTile; ++e)
               mx[e] = fmaxf(fmaxf(mx[e], s[k + 2 * e]), s[k + 2 * e + 1]);
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if constexpr (kSplit == 2) top = fmaxf(top, exchange(top, turn));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           if (tile == g.tile0) {
             m = top;
           } else {
             const bool rise = top > -kInf && (m == -kInf || (top - m) * c > kRescale);
             if (__any_sync(~0u, rise)) {
               const float f = top > m ? ex2((m - top) * c) : 1.0f;
-              mbar_wait(obar, turn ^ 1, timed_out);
-              __syncwarp();
-              tmem_fence_after();
+              wait_o(tiles - 1);
 #pragma unroll
-              for (int k = 0; k < kOut; k += 16) {
+              for (int k = 0; k < DP; k += 16) {
                 uint32_t o[16];
                 tmem_ld16(o_at + k, o);
                 tmem_wait_ld();
@@ -702,13 +649,13 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           if (__any_sync(~0u, fabsf(base) > 0x1p20f)) {
             // scores so large that the rounding of m c would not cancel in s c - m c
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) s[k] = (s[k] - (m == -kInf ? 0.0f : m)) * c;
+            for (int k = 0; k < kTile; ++k) s[k] = (s[k] - (m == -kInf ? 0.0f : m)) * c;
             base = 0.0f, mul = 1.0f;
           }
           const uint64_t mul2 = pack2(mul, mul), base2 = pack2(-base, -base);
           uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int k = 0; k < kCols; k += 32) {
+          for (int k = 0; k < kTile; k += 32) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -718,41 +665,36 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
               sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(p1), "f"(p0));
             }
-            tmem_st16(s_at + (part * kCols + k) / 2, w);
+            tmem_st16(s_at + buf * kTile + k / 2, w);
           }
           float s0, s1;
           unpack2(add2(sum[0], sum[1]), &s0, &s1);
           l += s0 + s1;
           tmem_wait_st();
-        } else if constexpr (kSplit == 2) {
-          named_bar_sync(1 + st, 256);
         }
         tmem_fence_before();
-        mbar_arrive(pbar);
-        turn ^= 1;
-        ring_step(L::kPerTile);
+        mbar_arrive(smem_addr(&bars->p[st][buf]));
       }
+      u0 += 2 * (g.tile1 - g.tile0);
+      turn0 ^= (u0 / L::kUnits) & 1;
+      u0 %= L::kUnits;
 
       if (live) {
         // ------------------------------------------------------ epilogue
-        if constexpr (kSplit == 2) l += exchange(l, turn);
-        mbar_wait(obar, turn ^ 1, timed_out);
-        __syncwarp();
-        tmem_fence_after();
+        wait_o(tiles - 1);
         if (work) {
-          const bool valid = st * kTile + row < g.rows;
+          const bool valid = st * kRows + row < g.rows;
           const bool odd = *reinterpret_cast<volatile int32_t*>(&bars->odd) != 0;
-          const int i = g.m * MR + st * kTile + row;
+          const int i = g.m * MR + st * kRows + row;
           const int head = g.h * a.group + i % a.group;
           const int64_t orow = g.row0 + i / a.group;
           const int slot = 2 * blockIdx.x + (g.begins ? 1 : 0);
           const float inv = g.whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
-          const int prow = st * kTile + row;
+          const int prow = st * kRows + row;
 #pragma unroll 1
-          for (int k0 = 0; k0 < kOut; k0 += 16) {
-            const int k = part * kOut + k0;
+          for (int k = 0; k < DP; k += 16) {
             uint32_t x[16];
-            tmem_ld16(o_at + k0, x);
+            tmem_ld16(o_at + k, x);
             tmem_wait_ld();
             float* o = reinterpret_cast<float*>(x);
             __syncwarp();
@@ -791,7 +733,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
                     make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
-          if (valid && part == 0) {
+          if (valid) {
             const float mc = m == -kInf ? -kInf : m * c;
             if (!g.whole)
               p.ml[static_cast<int64_t>(slot) * MR + prow] = make_float2(mc, l);
