@@ -414,78 +414,86 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
     if (err != 0 && a.dev_error != nullptr) atomicOr(a.dev_error, static_cast<int32_t>(err));
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t kQk = mma_idesc(kTile, false), kPv = mma_idesc(DP, true);
-      int u = 0;
-      uint32_t turn = 0;                // parity of the ring's turn
-      uint32_t tiles[2] = {0, 0};       // each stream's S tiles so far
-      uint32_t done[2] = {0, 0};        // and P tiles
-      uint32_t qturn = 0;
-      auto step = [&]() {
-        if (++u == L::kUnits) u = 0, turn ^= 1;
-      };
-      // S of the streams [0, ns) from the K unit at u
-      auto qk = [&](int s, int unit) {
-        const uint32_t kb = ring_addr + unit * L::kUnitBytes, b = tiles[s] & 1;
+    // The whole warp walks; one lane issues.  What the instructions' operands are
+    // formed from is the same in all lanes, and shuffles say so to the compiler,
+    // which then keeps it in uniform registers: operands moved there one by one
+    // took 80 cycles an instruction, against 48 (Q K^T, bound by reading Q and K
+    // from shared memory) and 64 (P V) of the products.
+    constexpr uint32_t kQk = mma_idesc(kTile, false), kPv = mma_idesc(DP, true);
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    int u = 0;
+    uint32_t turn = 0;           // parity of the ring's turn
+    uint32_t tiles[2] = {0, 0};  // each stream's S tiles so far
+    uint32_t done[2] = {0, 0};   // and P tiles
+    uint32_t qturn = 0;
+    auto step = [&]() {
+      if (++u == L::kUnits) u = 0, turn ^= 1;
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      mbar_wait(bar, parity, timed_out);
+      __syncwarp();
+      tmem_fence_after();
+    };
+    const uint64_t qdesc = smem_desc(q_addr, 0), kdesc = smem_desc(ring_addr, 0),
+                   vdesc = smem_desc(ring_addr, DP > 64 ? kTile * 128 : 0);
+    // S of stream s from the K unit at `unit`, which `last` gives back
+    auto qk = [&](int s, int unit, bool last) {
+      const uint32_t b = tiles[s] & 1, d = tm + (s * 2 + b) * kTile;
+      const uint64_t q = qdesc + s * (L::kQBytes / 16), k = kdesc + unit * (L::kUnitBytes / 16);
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t at = (k % 4) * 32;
-          mma_ss(tmem + (s * 2 + b) * kTile,
-                 smem_desc(q_addr + s * L::kQBytes + k / 4 * (kRows * 128) + at, 0),
-                 smem_desc(kb + k / 4 * (kTile * 128) + at, 0), kQk, k > 0);
-        }
-        ++tiles[s];
-        return smem_addr(&bars->s[s][b]);
-      };
-      Segment g;
-      while (walk.next(p, &g)) {
-        const int ns = NS == 2 && g.rows > kRows ? 2 : 1, n = g.tile1 - g.tile0;
-        for (int s = 0; s < NS; ++s) mbar_wait(smem_addr(&bars->q[s]), qturn, timed_out);
-        qturn ^= 1;
-        if (ns < NS) mbar_arrive(smem_addr(&bars->idle));  // the second stream may go on
-        for (int i = 0; i < min(2, n); ++i) {
-          mbar_wait(full(u), turn, timed_out);
-          tmem_fence_after();
-          for (int s = 0; s < ns; ++s) {
-            const uint32_t ready = qk(s, u);
-            if (s == ns - 1) mma_commit(empty(u));
-            mma_commit(ready);
-          }
-          step();
-        }
-        for (int i = 0; i < n; ++i) {
-          const int vu = u;
-          const uint32_t vt = turn;
-          step();
-          const bool ahead = i + 2 < n;
-          for (int s = 0; s < ns; ++s) {
-            const uint32_t b = done[s] & 1;
-            mbar_wait(smem_addr(&bars->p[s][b]), done[s] >> 1 & 1, timed_out);
+        for (int i = 0; i < DP / 16; ++i)
+          mma_ss(d, q + (i / 4 * (kRows * 128) + i % 4 * 32) / 16,
+                 k + (i / 4 * (kTile * 128) + i % 4 * 32) / 16, kQk, i > 0);
+        if (last) mma_commit(empty(unit));
+        mma_commit(smem_addr(&bars->s[s][b]));
+      }
+      ++tiles[s];
+    };
+    Segment g;
+    while (true) {
+      const bool more = walk.next(p, &g);
+      const int n = __shfl_sync(~0u, more ? g.tile1 - g.tile0 : 0, 0);
+      if (n == 0) break;
+      const int ns = NS == 1 ? 1 : __shfl_sync(~0u, g.rows > kRows ? 2 : 1, 0);
+      for (int s = 0; s < NS; ++s) wait(smem_addr(&bars->q[s]), qturn);
+      qturn ^= 1;
+      if (ns < NS && lane == 0) mbar_arrive(smem_addr(&bars->idle));  // the second stream may go on
+      for (int i = 0; i < min(2, n); ++i) {
+        wait(full(u), turn);
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          if (s < ns) qk(s, u, s == ns - 1);
+        step();
+      }
+      for (int i = 0; i < n; ++i) {
+        const int vu = u;
+        const uint32_t vt = turn;
+        step();
+        const bool ahead = i + 2 < n;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          if (s < ns) {
+            const uint32_t b = done[s] & 1, d = tm + kO + s * DP, pt = tm + (s * 2 + b) * kTile;
+            const uint64_t v = vdesc + vu * (L::kUnitBytes / 16);
+            wait(smem_addr(&bars->p[s][b]), done[s] >> 1 & 1);
             ++done[s];
-            if (s == 0) mbar_wait(full(vu), vt, timed_out);
-            tmem_fence_after();
+            if (s == 0) wait(full(vu), vt);
+            if (elect_one()) {
+              mma_ts(d, pt, v, kPv, i > 0);
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(tmem + kO + s * DP, tmem + (s * 2 + b) * kTile + k * 8,
-                     smem_desc(ring_addr + vu * L::kUnitBytes + k * 2048, DP > 64 ? kTile * 128 : 0),
-                     kPv, i > 0 || k > 0);
-            if (s == ns - 1) mma_commit(empty(vu));
-            mma_commit(smem_addr(&bars->o[s][b]));
+              for (int k = 1; k < kTile / 16; ++k) mma_ts(d, pt + k * 8, v + k * (2048 / 16), kPv, true);
+              if (s == ns - 1) mma_commit(empty(vu));
+              mma_commit(smem_addr(&bars->o[s][b]));
+            }
             if (ahead) {
-              if (s == 0) {
-                mbar_wait(full(u), turn, timed_out);
-                tmem_fence_after();
-              }
-              const uint32_t ready = qk(s, u);
-              if (s == ns - 1) mma_commit(empty(u));
-              mma_commit(ready);
+              if (s == 0) wait(full(u), turn);
+              qk(s, u, s == ns - 1);
             }
           }
-          if (ahead) step();
-        }
+        if (ahead) step();
       }
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------- softmax
     const int st = warp >> 2;          // stream

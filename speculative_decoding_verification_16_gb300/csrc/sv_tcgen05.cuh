@@ -61,17 +61,26 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // ---------------------------------------------------------------- products
 // Shared-memory operand in 128-byte rows with the 128-byte swizzle (16-byte
 // unit j of row r at unit j ^ (r & 7)); rows are packed in groups of eight,
-// 1024 bytes apart.  `lead`: bytes between 64-element column chunks of an
-// operand whose rows run along K (0 where the instruction needs one chunk).
+// 1024 bytes apart.  To a descriptor (bytes >> 4) may be added.  `lead`: bytes
+// between 64-element column chunks of an operand whose rows run along K (0 where
+// the instruction needs one chunk).
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | static_cast<uint64_t>((lead >> 4) & 0x3fff) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+  return static_cast<uint64_t>(1024 >> 4 | 1u << 14 | 2u << 29) << 32 | (addr >> 4 | (lead >> 4) << 16);
 }
 // bf16 x bf16 -> fp32, M = 128.
 __host__ __device__ constexpr uint32_t mma_idesc(int n, bool b_rows_along_k) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (b_rows_along_k ? 1u << 16 : 0u) |
          static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(128 >> 4) << 24;
 }
+// Non-zero in one lane of a warp that runs this together.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on;
+}
+// The instructions below are for one lane of a warp, in a branch of its own.
 // D[tmem] (+)= A[smem] B[smem], K = 16.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -88,7 +97,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
-// One arrival on the barrier when this thread's products so far are done.
+// One arrival on the barrier when this lane's products so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
