@@ -69,7 +69,7 @@ struct MmaArgs {
 
 constexpr int kMaxUnits = 10;
 __host__ __device__ constexpr int attn_units(int ns, int dp) { return ns == 1 && dp == 128 ? 5 : kMaxUnits; }
-__host__ __device__ constexpr int attn_threads(int ns) { return (ns * 4 + 2) * 32; }
+__host__ __device__ constexpr int attn_threads(int ns) { return (ns * 4 + 1 + ns) * 32; }
 // query tiles, ring of key and value tiles, barriers, the softmax warps' walks
 __host__ __device__ constexpr int attn_smem(int ns, int dp) {
   return ns * kRows * dp * 2 + attn_units(ns, dp) * kTile * dp * 2 + 320 + ns * 4 * 104;
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   if (tid == 0) {
     for (int i = 0; i < L::kUnits; ++i) {
       mbar_init(smem_addr(&bars->full[i]), TMA ? 1 : 32);
-      mbar_init(smem_addr(&bars->empty[i]), 1);
+      mbar_init(smem_addr(&bars->empty[i]), NS);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_addr(&bars->q[s]), 128);
@@ -412,19 +412,23 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       }
     }
     if (err != 0 && a.dev_error != nullptr) atomicOr(a.dev_error, static_cast<int32_t>(err));
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // ---------------------------------------------------------- products
-    // The whole warp walks; one lane issues.  What the instructions' operands are
-    // formed from is the same in all lanes, and shuffles say so to the compiler,
-    // which then keeps it in uniform registers: operands moved there one by one
-    // took 80 cycles an instruction, against 48 (Q K^T, bound by reading Q and K
-    // from shared memory) and 64 (P V) of the products.
+    // One warp a stream: a wait takes some 150 cycles even where the phase is
+    // over, and one warp for both streams spent more time in waits and issue than
+    // the products take.  The whole warp walks, one lane issues.  What the
+    // instructions' operands are formed from is the same in all lanes, and
+    // shuffles say so to the compiler, which then keeps it in uniform registers:
+    // operands moved there one by one took 80 cycles an instruction, against 48
+    // (Q K^T, bound by reading Q and K from shared memory) and 64 (P V) of the
+    // products themselves.
     constexpr uint32_t kQk = mma_idesc(kTile, false), kPv = mma_idesc(DP, true);
-    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    const int s = __shfl_sync(~0u, warp - kMmaWarp, 0);
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0) + s * 2 * kTile,
+                   to = __shfl_sync(~0u, tmem, 0) + kO + s * DP;
     int u = 0;
-    uint32_t turn = 0;           // parity of the ring's turn
-    uint32_t tiles[2] = {0, 0};  // each stream's S tiles so far
-    uint32_t done[2] = {0, 0};   // and P tiles
+    uint32_t turn = 0;                     // parity of the ring's turn
+    uint32_t tiles = 0, done = 0;          // the stream's S and P tiles so far
     uint32_t qturn = 0;
     auto step = [&]() {
       if (++u == L::kUnits) u = 0, turn ^= 1;
@@ -434,64 +438,62 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       __syncwarp();
       tmem_fence_after();
     };
-    const uint64_t qdesc = smem_desc(q_addr, 0), kdesc = smem_desc(ring_addr, 0),
+    const uint64_t qdesc = smem_desc(q_addr, 0) + s * (L::kQBytes / 16),
+                   kdesc = smem_desc(ring_addr, 0),
                    vdesc = smem_desc(ring_addr, DP > 64 ? kTile * 128 : 0);
-    // S of stream s from the K unit at `unit`, which `last` gives back
-    auto qk = [&](int s, int unit, bool last) {
-      const uint32_t b = tiles[s] & 1, d = tm + (s * 2 + b) * kTile;
-      const uint64_t q = qdesc + s * (L::kQBytes / 16), k = kdesc + unit * (L::kUnitBytes / 16);
+    auto qk = [&]() {  // S from the K unit at u
+      const uint32_t b = tiles & 1, d = tm + b * kTile;
+      const uint64_t k = kdesc + u * (L::kUnitBytes / 16);
       if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i)
-          mma_ss(d, q + (i / 4 * (kRows * 128) + i % 4 * 32) / 16,
+          mma_ss(d, qdesc + (i / 4 * (kRows * 128) + i % 4 * 32) / 16,
                  k + (i / 4 * (kTile * 128) + i % 4 * 32) / 16, kQk, i > 0);
-        if (last) mma_commit(empty(unit));
+        mma_commit(empty(u));
         mma_commit(smem_addr(&bars->s[s][b]));
       }
-      ++tiles[s];
+      ++tiles;
+      step();
     };
     Segment g;
     while (true) {
       const bool more = walk.next(p, &g);
       const int n = __shfl_sync(~0u, more ? g.tile1 - g.tile0 : 0, 0);
       if (n == 0) break;
-      const int ns = NS == 1 ? 1 : __shfl_sync(~0u, g.rows > kRows ? 2 : 1, 0);
-      for (int s = 0; s < NS; ++s) wait(smem_addr(&bars->q[s]), qturn);
+      wait(smem_addr(&bars->q[s]), qturn);
       qturn ^= 1;
-      if (ns < NS && lane == 0) mbar_arrive(smem_addr(&bars->idle));  // the second stream may go on
+      if (s > 0 && __shfl_sync(~0u, g.rows <= kRows ? 1 : 0, 0)) {
+        // no rows in this stream: its part in the ring, and its softmax may go on
+        if (lane == 0) mbar_arrive(smem_addr(&bars->idle));
+        for (int i = 0; i < 2 * n; ++i) {
+          wait(full(u), turn);
+          if (lane == 0) mbar_arrive(empty(u));
+          step();
+        }
+        continue;
+      }
       for (int i = 0; i < min(2, n); ++i) {
         wait(full(u), turn);
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-          if (s < ns) qk(s, u, s == ns - 1);
-        step();
+        qk();
       }
       for (int i = 0; i < n; ++i) {
-        const int vu = u;
-        const uint32_t vt = turn;
+        const uint32_t b = done & 1, pt = tm + b * kTile;
+        const uint64_t v = vdesc + u * (L::kUnitBytes / 16);
+        wait(full(u), turn);
+        wait(smem_addr(&bars->p[s][b]), done >> 1 & 1);
+        ++done;
+        if (elect_one()) {
+          mma_ts(to, pt, v, kPv, i > 0);
+#pragma unroll
+          for (int k = 1; k < kTile / 16; ++k) mma_ts(to, pt + k * 8, v + k * (2048 / 16), kPv, true);
+          mma_commit(empty(u));
+          mma_commit(smem_addr(&bars->o[s][b]));
+        }
         step();
-        const bool ahead = i + 2 < n;
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-          if (s < ns) {
-            const uint32_t b = done[s] & 1, d = tm + kO + s * DP, pt = tm + (s * 2 + b) * kTile;
-            const uint64_t v = vdesc + vu * (L::kUnitBytes / 16);
-            wait(smem_addr(&bars->p[s][b]), done[s] >> 1 & 1);
-            ++done[s];
-            if (s == 0) wait(full(vu), vt);
-            if (elect_one()) {
-              mma_ts(d, pt, v, kPv, i > 0);
-#pragma unroll
-              for (int k = 1; k < kTile / 16; ++k) mma_ts(d, pt + k * 8, v + k * (2048 / 16), kPv, true);
-              if (s == ns - 1) mma_commit(empty(vu));
-              mma_commit(smem_addr(&bars->o[s][b]));
-            }
-            if (ahead) {
-              if (s == 0) wait(full(u), turn);
-              qk(s, u, s == ns - 1);
-            }
-          }
-        if (ahead) step();
+        if (i + 2 < n) {
+          wait(full(u), turn);
+          qk();
+        }
       }
     }
   } else {
