@@ -218,9 +218,11 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
   if (rc != SV_OK) return rc;
   const int dp = a.dim <= 64 ? 64 : 128;
   char* ws = static_cast<char*>(workspace);
-  MmaArgs p{a, kv_heads, 0, reinterpret_cast<AttnRecord*>(ws),
+  MmaArgs p{a, kv_heads, 0, -1, reinterpret_cast<AttnRecord*>(ws),
             reinterpret_cast<float2*>(ws + kRecordBytes),
             reinterpret_cast<float4*>(ws + kRecordBytes + kMlBytes)};
+  for (int i = 0; i < 31; ++i)
+    if (a.page == 1 << i) p.page_shift = i;
   // whole page pieces by tensor copies where pages hold a number of them and
   // the strides fit a tensor map
   p.box = a.page % 64 == 0 ? 64 : a.page == 8 || a.page == 16 || a.page == 32 ? a.page : 0;

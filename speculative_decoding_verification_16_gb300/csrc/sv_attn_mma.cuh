@@ -62,6 +62,7 @@ struct AttnRecord {  // where a worker's run starts inside an item (off > 0)
 struct MmaArgs {
   AttnArgs a;
   int32_t kv_heads, box;  // box: tokens of a tensor copy; 0: copies of single rows
+  int32_t page_shift;     // log2 of the page size, -1 for another
   AttnRecord* record;     // [kMaxWorkers]
   float2* ml;             // [2 * kMaxWorkers][rows]: m c and l of the partials
   float4* o;              // [2 * kMaxWorkers][DP / 4][rows]
@@ -69,7 +70,7 @@ struct MmaArgs {
 
 constexpr int kMaxUnits = 10;
 __host__ __device__ constexpr int attn_units(int ns, int dp) { return ns == 1 && dp == 128 ? 5 : kMaxUnits; }
-__host__ __device__ constexpr int attn_threads(int ns) { return (ns * 4 + 1 + ns) * 32; }
+__host__ __device__ constexpr int attn_threads(int ns) { return ns * 6 * 32; }  // softmax, copies, products
 // query tiles, ring of key and value tiles, barriers, the softmax warps' walks
 __host__ __device__ constexpr int attn_smem(int ns, int dp) {
   return ns * kRows * dp * 2 + attn_units(ns, dp) * kTile * dp * 2 + 320 + ns * 4 * 104;
@@ -242,7 +243,8 @@ struct AttnBars {
 static_assert(sizeof(AttnBars) <= 320, "barrier block");
 
 // The ring's order in a segment of n tiles is that of the products: K 0, K 1,
-// V 0, K 2, V 1, K 3, ..  Position of the V of tile i:
+// V 0, K 2, V 1, K 3, ..  Positions of the K and the V of tile i:
+__device__ __forceinline__ int k_position(int i) { return i < 2 ? i : 2 * i - 1; }
 __device__ __forceinline__ int v_position(int n, int i) { return min(n, i + 2) + i; }
 
 // Two floats at once: a * b + c and a + b.
@@ -289,7 +291,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   WarpWalk<MR>* const walks = reinterpret_cast<WarpWalk<MR>*>(reinterpret_cast<char*>(bars) + 320);
   static_assert(sizeof(WarpWalk<MR>) <= 104, "walk block");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kSoftmax = NS * 4, kLoadWarp = kSoftmax, kMmaWarp = kSoftmax + 1;
+  constexpr int kSoftmax = NS * 4, kLoadWarp = kSoftmax, kMmaWarp = kSoftmax + NS;
   bool timed_out = false;
 
   Walk<MR> walk;
@@ -323,43 +325,87 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   auto full = [&](int u) { return smem_addr(&bars->full[u]); };
   auto empty = [&](int u) { return smem_addr(&bars->empty[u]); };
 
-  if (warp == kLoadWarp) {
+  if (warp >= kLoadWarp && warp < kMmaWarp) {
     // ---------------------------------------------------------- copies
-    int u = 0;          // ring position
-    uint32_t turn = 0;  // parity of the ring's turn
-    int issued = 0;     // units issued so far
+    int before = 0;  // units of the segments so far
     uint32_t err = 0;
     Segment g;
-    while (walk.next(p, &g)) {
-      const int32_t* table = a.table + g.r * a.table_stride;
-      const int n = g.tile1 - g.tile0;
-      int ki = 0, vi = 0;
-      for (int x = 0; x < 2 * n; ++x) {
-        // K 0, K 1, then V and K in turn until the Ks are through
-        const bool val = ki == n || (ki >= 2 && ki == vi + 2);
-        const int t0 = (g.tile0 + (val ? vi++ : ki++)) * kTile;
-        const uint32_t dst = ring_addr + u * L::kUnitBytes;
-        if constexpr (TMA) {
-          // lane: box lane / chunks of the unit, column chunk lane % chunks
-          const int boxes = kTile / p.box;
-          const int t = t0 + lane / L::kChunks * p.box, c = lane % L::kChunks;
-          const bool on = lane < boxes * L::kChunks && t < g.kv_end;
+    if constexpr (TMA) {
+      // NS = 1: one warp copies K and V in the ring's order; NS = 2: one the Ks,
+      // one the Vs (one for both took 1,000 cycles a unit, of which a pair of
+      // tiles has two in some 1,300).  The page ids are loaded one unit ahead,
+      // lane b those of the unit's box b; one lane issues the copies.
+      const int side = __shfl_sync(~0u, warp - kLoadWarp, 0);
+      const int boxes = kTile / p.box;
+      const uint32_t bytes = static_cast<uint32_t>(p.box) * L::kChunks * 128;
+      while (true) {
+        const bool more = walk.next(p, &g);
+        const int n = __shfl_sync(~0u, more ? g.tile1 - g.tile0 : 0, 0);
+        if (n == 0) break;
+        const int tile0 = __shfl_sync(~0u, g.tile0, 0), end = __shfl_sync(~0u, g.kv_end, 0),
+                  head = __shfl_sync(~0u, g.h, 0);
+        const int32_t* table = a.table + g.r * a.table_stride;
+        auto load_id = [&](int t0) {
+          const int t = t0 + lane * p.box;
           int id = 0;
-          if (on) {
-            id = __ldg(table + t / a.page);
+          if (lane < boxes && t < end) {
+            id = __ldg(table + (p.page_shift >= 0 ? t >> p.page_shift : t / a.page));
             if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
           }
-          const unsigned live = __ballot_sync(~0u, on);
-          if (issued >= L::kUnits) mbar_wait(empty(u), turn ^ 1, timed_out);
-          if (lane == 0)
-            mbar_arrive_expect_tx(full(u), static_cast<uint32_t>(__popc(live)) * p.box * 128);
+          return id;
+        };
+        const int count = NS == 1 ? 2 * n : n;
+        int ki = 0, vi = 0;
+        // the warp's next unit: whether it is a V, its tile's first key, its place
+        auto order = [&](bool* val, int* at) {
+          *val = NS == 2 ? side == 1 : ki == n || (ki >= 2 && ki == vi + 2);
+          const int i = *val ? vi++ : ki++;
+          *at = before + (*val ? v_position(n, i) : k_position(i));
+          return (tile0 + i) * kTile;
+        };
+        bool val, val_next = false;
+        int at, at_next = 0, t0 = order(&val, &at), t_next = 0, id = load_id(t0), id_next = 0;
+        for (int x = 0; x < count; ++x) {
+          if (x + 1 < count) t_next = order(&val_next, &at_next), id_next = load_id(t_next);
+          const int u = at % L::kUnits;
+          if (at >= L::kUnits) mbar_wait(empty(u), (at / L::kUnits + 1) & 1, timed_out);
           __syncwarp();
-          if (on)
-            tma_load4(dst + c * (kTile * 128) + (t - t0) * 128, val ? &vmap : &kmap, c * 64,
-                      t % a.page, g.h, id, full(u));
-        } else {
-          // lane: the addresses of rows lane and lane + 32; 16-byte pieces
-          constexpr int kPieces = DP / 8;
+          const int live = max(0, min(boxes, (end - t0 + p.box - 1) / p.box));
+          if (elect_one()) mbar_arrive_expect_tx(full(u), live * bytes);
+          for (int b = 0; b < live; ++b) {
+            const int page = __shfl_sync(~0u, id, b), t = t0 + b * p.box;
+            const int in_page = p.page_shift >= 0 ? t & ((1 << p.page_shift) - 1) : t % a.page;
+            const uint32_t dst = ring_addr + u * L::kUnitBytes + b * p.box * 128;
+            if (elect_one()) {
+#pragma unroll
+              for (int c = 0; c < L::kChunks; ++c)
+                tma_load4(dst + c * (kTile * 128), val ? &vmap : &kmap, c * 64, in_page, head, page,
+                          full(u));
+            }
+          }
+          t0 = t_next, val = val_next, at = at_next, id = id_next;
+        }
+        before += 2 * n;
+      }
+      if (timed_out) {  // no copy outlives the CTA
+        for (int i = 0; i < L::kUnits && i < before; ++i) {
+          const int at = before - 1 - i;
+          bool late = false;
+          mbar_wait(full(at % L::kUnits), (at / L::kUnits) & 1, late);
+        }
+      }
+    } else if (warp == kLoadWarp) {
+      // rows copied one by one, 16 bytes a lane: lane's addresses are those of rows
+      // lane and lane + 32
+      int issued = 0;
+      constexpr int kPieces = DP / 8;
+      while (walk.next(p, &g)) {
+        const int32_t* table = a.table + g.r * a.table_stride;
+        const int n = g.tile1 - g.tile0;
+        int ki = 0, vi = 0;
+        for (int x = 0; x < 2 * n; ++x, ++issued) {
+          const bool val = ki == n || (ki >= 2 && ki == vi + 2);
+          const int t0 = (g.tile0 + (val ? vi++ : ki++)) * kTile, u = issued % L::kUnits;
           const char* at[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -371,8 +417,9 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
               at[k] = (val ? a.v : a.k) + id * a.block + (t % a.page) * a.token + g.h * a.head;
             }
           }
-          if (issued >= L::kUnits) mbar_wait(empty(u), turn ^ 1, timed_out);
+          if (issued >= L::kUnits) mbar_wait(empty(u), (issued / L::kUnits + 1) & 1, timed_out);
           __syncwarp();
+          const uint32_t dst = ring_addr + u * L::kUnitBytes;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             for (int i = 0; i < kPieces; ++i) {
@@ -389,27 +436,18 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           if (issued >= 2) {
             cp_async_wait<2>();
             fence_async_smem();
-            mbar_arrive(full((u + L::kUnits - 2) % L::kUnits));
+            mbar_arrive(full((issued - 2) % L::kUnits));
           }
         }
-        ++issued;
-        if (++u == L::kUnits) u = 0, turn ^= 1;
       }
-    }
-    if constexpr (!TMA) {
       if (issued >= 2) {
         cp_async_wait<1>();
         fence_async_smem();
-        mbar_arrive(full((u + L::kUnits - 2) % L::kUnits));
+        mbar_arrive(full((issued - 2) % L::kUnits));
       }
       cp_async_wait<0>();
       fence_async_smem();
-      mbar_arrive(full((u + L::kUnits - 1) % L::kUnits));
-    } else if (timed_out) {  // no copy outlives the CTA
-      for (int i = 0; i < L::kUnits; ++i) {
-        bool late = false;
-        mbar_wait(full(i), turn ^ (i < u ? 0u : 1u), late);
-      }
+      mbar_arrive(full((issued - 1) % L::kUnits));
     }
     if (err != 0 && a.dev_error != nullptr) atomicOr(a.dev_error, static_cast<int32_t>(err));
   } else if (warp >= kMmaWarp) {
