@@ -372,16 +372,23 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           __syncwarp();
           const int live = max(0, min(boxes, (end - t0 + p.box - 1) / p.box));
           if (elect_one()) mbar_arrive_expect_tx(full(u), live * bytes);
-          for (int b = 0; b < live; ++b) {
-            const int page = __shfl_sync(~0u, id, b), t = t0 + b * p.box;
-            const int in_page = p.page_shift >= 0 ? t & ((1 << p.page_shift) - 1) : t % a.page;
-            const uint32_t dst = ring_addr + u * L::kUnitBytes + b * p.box * 128;
-            if (elect_one()) {
+          const uint32_t dst = ring_addr + u * L::kUnitBytes;
+          if (boxes == 1) {
+            const int page = __shfl_sync(~0u, id, 0);
+            const int in_page = p.page_shift >= 0 ? t0 & ((1 << p.page_shift) - 1) : t0 % a.page;
+            if (live > 0 && elect_one()) {
 #pragma unroll
               for (int c = 0; c < L::kChunks; ++c)
                 tma_load4(dst + c * (kTile * 128), val ? &vmap : &kmap, c * 64, in_page, head, page,
                           full(u));
             }
+          } else {  // several small pages: a lane a copy
+            const int b = lane / L::kChunks, c = lane % L::kChunks;
+            const int page = __shfl_sync(~0u, id, b);
+            __syncwarp();
+            if (b < live)
+              tma_load4(dst + c * (kTile * 128) + b * p.box * 128, val ? &vmap : &kmap, c * 64, 0, head,
+                        page, full(u));
           }
           t0 = t_next, val = val_next, at = at_next, id = id_next;
         }
