@@ -208,8 +208,11 @@ int launch_mma(const MmaArgs& p, int grid, const CUtensorMap& km, const CUtensor
                ? launch(attn_mma_kernel<NS, DP, true>, dim3(grid), threads, smem, 1, false, st, p, km, vm)
                : launch(attn_mma_kernel<NS, DP, false>, dim3(grid), threads, smem, 1, false, st, p, km, vm);
   if (rc != SV_OK || grid == 1) return rc;  // one worker cuts no item
-  return launch(attn_combine_kernel<NS * kRows, DP>, dim3(grid, NS * kRows / kCombineRows),
-                kCombineThreads, 0, 1, true, st, p);
+  Device d;
+  rc = device(&d);
+  if (rc != SV_OK) return rc;
+  return launch(attn_combine_kernel<NS * kRows, DP>, dim3(16 * d.sms), kCombineThreads, 0, 1, true, st,
+                p, grid);
 }
 
 int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {

@@ -53,10 +53,9 @@ constexpr int kTile = 64;         // keys of a tile
 constexpr int kMaxWorkers = 320;  // partials are laid out for this many
 constexpr float kRescale = 8.0f;  // log2 of how far P may exceed 1 before O is rescaled
 
-struct AttnRecord {  // where a worker's run starts inside an item (off > 0)
-  int32_t r, h, m, off, n;  // item, tiles of it before the run, its tiles
-  int32_t workers;
-  int64_t total;  // all tiles
+struct AttnRecord {  // of a worker whose run is the second in an item
+  int32_t parts;  // runs that the item is cut into; 0 for another worker
+  int32_t rows, row0, h, m;  // the item's rows, its request's first row, head and row tile
 };
 
 struct MmaArgs {
@@ -180,7 +179,7 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem* sm, Walk<MR>* w
   total *= p.kv_heads;
   const int workers = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
   const int me = blockIdx.x;
-  AttnRecord rec{0, 0, 0, 0, 0, workers, total};
+  AttnRecord rec{0, 0, 0, 0, 0};
   bool any = me < workers;
   if (any) {
     const int64_t start = worker_start(total, workers, me);
@@ -219,7 +218,10 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem* sm, Walk<MR>* w
     while (rem >= n) rem -= n, n = item_tiles<MR>(a, w->s, ++w->m).n;
     w->off = static_cast<int>(rem);
     w->left = worker_start(total, workers, me + 1) - start;
-    rec.r = w->r, rec.h = w->h, rec.m = w->m, rec.off = w->off, rec.n = n;
+    const int64_t first = start - w->off;  // the item's first tile
+    if (w->off > 0 && worker_of(total, workers, first) == me - 1)
+      rec = AttnRecord{worker_of(total, workers, first + n - 1) - me + 2,
+                       item_tiles<MR>(a, w->s, w->m).rows, w->s.row0, w->h, w->m};
   }
   if (tid == 0) p.record[me] = rec;
   return any;
@@ -809,57 +811,117 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
 
 // ---------------------------------------------------------------- combine
 //
-// Joins the partials of the items that were cut: the block of a worker whose
-// run starts inside an item, if it is the first such worker, sums the item's
-// parts in worker order.  A thread a row, four columns at a time.
+// Joins the partials of the items that were cut.  Every block finds all of them
+// from the workers' records and takes four rows at a time: the parts' weights
+// 2^(m c - max) go to shared memory, then a thread sums four columns of a row
+// over the parts, in worker order.  Bound by the latency of two rounds of loads,
+// and by the partials' bytes (from L2) where there are many.
 constexpr int kCombineThreads = 128;
-constexpr int kCombineRows = 16;
+constexpr int kCombineRows = 4;
 
 template <int MR, int DP>
-__global__ __launch_bounds__(kCombineThreads) void attn_combine_kernel(const MmaArgs p) {
-  grid_dep_wait();
+__global__ __launch_bounds__(kCombineThreads) void attn_combine_kernel(const MmaArgs p, int workers) {
+  __shared__ AttnRecord item[kMaxWorkers];
+  __shared__ int32_t second[kMaxWorkers];  // the item's second worker
+  __shared__ float weight[kCombineRows][kMaxWorkers], inverse[kCombineRows];
+  __shared__ int32_t found[(kMaxWorkers + kCombineThreads - 1) / kCombineThreads * (kCombineThreads / 32)];
   const AttnArgs& a = p.a;
-  const int w = blockIdx.x;
-  const AttnRecord rec = p.record[w];
-  if (rec.off == 0) return;
-  const int64_t u0 = worker_start(rec.total, rec.workers, w) - rec.off;
-  const int w0 = worker_of(rec.total, rec.workers, u0);
-  if (w0 != w - 1) return;
-  const int w1 = worker_of(rec.total, rec.workers, u0 + rec.n - 1);
-  const Span s = span_of(a, rec.r);
-  const int rows = min(MR, s.l * a.group - rec.m * MR);
-  const int row = blockIdx.y * kCombineRows + (threadIdx.x % kCombineRows);
-  if (row >= rows) return;
-  float top = -kInf;
-  for (int i = w0; i <= w1; ++i)
-    top = fmaxf(top, p.ml[static_cast<int64_t>(2 * i + (i == w0 ? 1 : 0)) * MR + row].x);
-  const float base = top == -kInf ? 0.0f : top;
-  float l = 0;
-  for (int i = w0; i <= w1; ++i) {
-    const float2 x = p.ml[static_cast<int64_t>(2 * i + (i == w0 ? 1 : 0)) * MR + row];
-    l += x.y * ex2(x.x - base);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_wait();
+  // the list is in worker order, the same in every block
+  constexpr int kChunks = (kMaxWorkers + kCombineThreads - 1) / kCombineThreads;
+  constexpr int kWarps = kCombineThreads / 32;
+  AttnRecord mine[kChunks];
+  unsigned vote[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int w = c * kCombineThreads + tid;
+    mine[c] = w < workers ? p.record[w] : AttnRecord{0, 0, 0, 0, 0};
   }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  const int i = rec.m * MR + row;
-  const int64_t orow = s.row0 + i / a.group;
-  const int head = rec.h * a.group + i % a.group;
-  for (int q = threadIdx.x / kCombineRows; q < DP / 4; q += kCombineThreads / kCombineRows) {
-    if (q * 4 >= a.dim) break;
-    float4 o = make_float4(0, 0, 0, 0);
-    for (int j = w0; j <= w1; ++j) {
-      const int slot = 2 * j + (j == w0 ? 1 : 0);
-      const float f = ex2(p.ml[static_cast<int64_t>(slot) * MR + row].x - base);
-      const float4 x = p.o[(static_cast<int64_t>(slot) * (DP / 4) + q) * MR + row];
-      o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y);
-      o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    vote[c] = __ballot_sync(~0u, mine[c].parts > 0);
+    if (lane == 0) found[c * kWarps + warp] = __popc(vote[c]);
+  }
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp && mine[c].parts > 0) {
+        const int at = count + __popc(vote[c] & ((1u << lane) - 1));
+        item[at] = mine[c], second[at] = c * kCombineThreads + tid;
+      }
+      count += found[c * kWarps + w];
     }
-    uint2 v;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(o.y * inv), "f"(o.x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(o.w * inv), "f"(o.z * inv));
-    *reinterpret_cast<uint2*>(a.out + orow * a.o_row + head * a.o_head + q * 8) = v;
+  __syncthreads();
+  for (int task = blockIdx.x; task < count * (MR / kCombineRows); task += gridDim.x) {
+    const AttnRecord r = item[task % count];
+    const int w0 = second[task % count] - 1, row0 = task / count * kCombineRows;
+    const int rows = r.rows;
+    if (row0 >= rows) continue;
+    auto slot = [&](int i) { return static_cast<int64_t>(2 * (w0 + i) + (i == 0 ? 1 : 0)); };
+    // thread: row row0 + tid % 4, columns [4 q, 4 q + 4); the first parts' loads go
+    // out before the weights are known
+    const int sub = tid % kCombineRows, q = tid / kCombineRows, mine_row = row0 + sub;
+    const bool on = mine_row < rows && q * 4 < a.dim;
+    auto load = [&](int i) { return p.o[(slot(i) * (DP / 4) + q) * MR + mine_row]; };
+    float4 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (on && j < r.parts) x[j] = load(j);
+    __syncthreads();  // the weights of the task before are done with
+    if (row0 + warp < rows) {  // warp j: the weights of row row0 + j
+      const int row = row0 + warp;
+      float top = -kInf, l = 0.0f;
+      for (int i = lane; i < r.parts; i += 32) top = fmaxf(top, p.ml[slot(i) * MR + row].x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      if (top == -kInf) top = 0.0f;
+      for (int i = lane; i < r.parts; i += 32) {
+        const float2 x = p.ml[slot(i) * MR + row];
+        const float f = ex2(x.x - top);
+        weight[warp][i] = f;
+        l += x.y * f;
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+      if (lane == 0) {
+        inverse[warp] = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        const int j = r.m * MR + row;
+        if (a.lse != nullptr)
+          a.lse[(static_cast<int64_t>(r.row0) + j / a.group) * a.heads + r.h * a.group + j % a.group] =
+              l > 0.0f || l != l ? (top + log2f(l)) * kLn2 : -kInf;
+      }
+    }
+    __syncthreads();
+    if (on) {
+      float4 o = make_float4(0, 0, 0, 0);
+      for (int i = 0; i < r.parts; i += 8) {
+        if (i > 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (i + j < r.parts) x[j] = load(i + j);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < r.parts) {
+            const float f = weight[sub][i + j];
+            o.x = fmaf(x[j].x, f, o.x), o.y = fmaf(x[j].y, f, o.y);
+            o.z = fmaf(x[j].z, f, o.z), o.w = fmaf(x[j].w, f, o.w);
+          }
+      }
+      const float inv = inverse[sub];
+      const int j = r.m * MR + mine_row;
+      uint2 v;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(o.y * inv), "f"(o.x * inv));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(o.w * inv), "f"(o.z * inv));
+      const int64_t orow = static_cast<int64_t>(r.row0) + j / a.group;
+      const int head = r.h * a.group + j % a.group;
+      *reinterpret_cast<uint2*>(a.out + orow * a.o_row + head * a.o_head + q * 8) = v;
+    }
   }
-  if (threadIdx.x < kCombineRows && a.lse != nullptr)
-    a.lse[orow * a.heads + head] = l > 0.0f || l != l ? (base + log2f(l)) * kLn2 : -kInf;
 }
 
 }  // namespace serve
