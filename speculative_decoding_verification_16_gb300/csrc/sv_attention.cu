@@ -17,6 +17,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_huge_valf();
 
+// Division of 0 <= n < 2^31 by a fixed d: n / d = (mulhi(n, mul) + n) >> shift with
+// mul = 2^32 (2^shift - d) / d + 1, 2^shift >= d (Granlund and Montgomery 1994).
+struct FastDiv {
+  uint32_t mul, shift;
+  static FastDiv by(uint32_t d) {
+    uint32_t s = 0;
+    while ((uint64_t{1} << s) < d) ++s;
+    return FastDiv{static_cast<uint32_t>((((uint64_t{1} << s) - d) << 32) / d + 1), s};
+  }
+  __device__ __forceinline__ int of(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
+
 struct AttnArgs {
   const char* q;
   int64_t q_row, q_head;  // bytes
@@ -32,6 +46,7 @@ struct AttnArgs {
   int64_t o_row, o_head;  // bytes
   float* lse;
   int32_t* dev_error;
+  FastDiv by_group, by_page;
 };
 
 // Request r's rows and length, or l = -1 when they are out of range.
@@ -201,8 +216,8 @@ bool encode_cache(CUtensorMap* map, const void* base, const AttnArgs& a, int kv_
 }
 
 template <int NS, int DP>
-int launch_mma(const MmaArgs& p, int grid, const CUtensorMap& km, const CUtensorMap& vm,
-               cudaStream_t st) {
+int launch_mma(const MmaArgs& p, int grid, int64_t joins, const CUtensorMap& km,
+               const CUtensorMap& vm, cudaStream_t st) {
   constexpr int threads = attn_threads(NS), smem = attn_smem(NS, DP);
   int rc = p.box > 0
                ? launch(attn_mma_kernel<NS, DP, true>, dim3(grid), threads, smem, 1, false, st, p, km, vm)
@@ -211,7 +226,7 @@ int launch_mma(const MmaArgs& p, int grid, const CUtensorMap& km, const CUtensor
   Device d;
   rc = device(&d);
   if (rc != SV_OK) return rc;
-  return launch(attn_combine_kernel<NS * kRows, DP>, dim3(16 * d.sms), kCombineThreads, 0, 1, true, st,
+  return launch(attn_combine_kernel<NS * kRows, DP>, dim3(static_cast<unsigned>(std::min<int64_t>(joins, 16 * d.sms))), kCombineThreads, 0, 1, true, st,
                 p, grid);
 }
 
@@ -221,11 +236,9 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
   if (rc != SV_OK) return rc;
   const int dp = a.dim <= 64 ? 64 : 128;
   char* ws = static_cast<char*>(workspace);
-  MmaArgs p{a, kv_heads, 0, -1, reinterpret_cast<AttnRecord*>(ws),
+  MmaArgs p{a, kv_heads, 0, reinterpret_cast<AttnRecord*>(ws),
             reinterpret_cast<float2*>(ws + kRecordBytes),
             reinterpret_cast<float4*>(ws + kRecordBytes + kMlBytes)};
-  for (int i = 0; i < 31; ++i)
-    if (a.page == 1 << i) p.page_shift = i;
   // whole page pieces by tensor copies where pages hold a number of them and
   // the strides fit a tensor map
   p.box = a.page % 64 == 0 ? 64 : a.page == 8 || a.page == 16 || a.page == 32 ? a.page : 0;
@@ -245,9 +258,13 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
                         a.B * kv_heads;
   const int64_t most = ns == 1 ? std::min(2 * d.sms, kMaxWorkers) : std::min(d.sms, kMaxWorkers / 2);
   const int grid = static_cast<int>(std::min(most, tiles));
+  // row groups of the items that can be cut: a block each, up to 16 an SM
+  const int64_t items = (rows + ns * kRows - 1) / (ns * kRows) * a.B * kv_heads;
+  const int64_t joins = std::min<int64_t>(items, grid - 1) *
+                        ((std::min<int64_t>(rows, ns * kRows) + kCombineRows - 1) / kCombineRows);
   if (ns == 1)
-    return dp == 64 ? launch_mma<1, 64>(p, grid, km, vm, st) : launch_mma<1, 128>(p, grid, km, vm, st);
-  return dp == 64 ? launch_mma<2, 64>(p, grid, km, vm, st) : launch_mma<2, 128>(p, grid, km, vm, st);
+    return dp == 64 ? launch_mma<1, 64>(p, grid, joins, km, vm, st) : launch_mma<1, 128>(p, grid, joins, km, vm, st);
+  return dp == 64 ? launch_mma<2, 64>(p, grid, joins, km, vm, st) : launch_mma<2, 128>(p, grid, joins, km, vm, st);
 }
 
 }  // namespace
@@ -309,7 +326,8 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
                    heads / kv_heads, head_dim, num_blocks, page_size, window,
                    c == 0.0f ? 1e-37f : c,  // masked scores stay -inf
                    static_cast<char*>(out), o_row_stride * es, o_head_stride * es, out_lse,
-                   dev_error};
+                   dev_error, FastDiv::by(static_cast<uint32_t>(heads / kv_heads)),
+                   FastDiv::by(static_cast<uint32_t>(page_size))};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (on_tensor_cores(dtype, head_dim)) return run_mma(a, kv_heads, workspace, st);
   const int64_t items = static_cast<int64_t>(n_rows) * heads;

@@ -61,7 +61,6 @@ struct AttnRecord {  // of a worker whose run is the second in an item
 struct MmaArgs {
   AttnArgs a;
   int32_t kv_heads, box;  // box: tokens of a tensor copy; 0: copies of single rows
-  int32_t page_shift;     // log2 of the page size, -1 for another
   AttnRecord* record;     // [kMaxWorkers]
   float2* ml;             // [2 * kMaxWorkers][rows]: m c and l of the partials
   float4* o;              // [2 * kMaxWorkers][DP / 4][rows]
@@ -94,7 +93,7 @@ __device__ __forceinline__ ItemTiles item_tiles(const AttnArgs& a, const Span& s
   ItemTiles t;
   const int all = s.l * a.group;
   t.rows = min(MR, all - m * MR);
-  const int j0 = m * MR / a.group, j1 = (m * MR + t.rows - 1) / a.group;
+  const int j0 = a.by_group.of(m * MR), j1 = a.by_group.of(m * MR + t.rows - 1);
   t.kv_end = max(0, s.seq - s.l + j1 + 1);
   const int kv_lo = a.window > 0 ? max(0, s.seq - s.l + j0 - a.window + 1) : 0;
   t.lo = kv_lo / kTile;
@@ -110,10 +109,16 @@ __device__ __forceinline__ int64_t head_tiles(const AttnArgs& a, const Span& s) 
   return n;
 }
 
+// Products with up to kMaxWorkers fit 32 bits below this total: 64-bit division
+// takes hundreds of cycles.
+constexpr int64_t kSmallTotal = int64_t{1} << 22;
 __device__ __forceinline__ int64_t worker_start(int64_t total, int workers, int w) {
+  if (total < kSmallTotal) return static_cast<uint32_t>(total) * w / static_cast<uint32_t>(workers);
   return total * w / workers;
 }
 __device__ __forceinline__ int worker_of(int64_t total, int workers, int64_t u) {
+  if (total < kSmallTotal)
+    return static_cast<int>((static_cast<uint32_t>(u + 1) * workers - 1) / static_cast<uint32_t>(total));
   return static_cast<int>(((u + 1) * workers - 1) / total);
 }
 
@@ -147,84 +152,103 @@ struct Walk {  // a worker's segments in order
   }
 };
 
+template <int MR>
 struct PlanSmem {
   int64_t part[16];
-  int64_t total;
-  int64_t rem;
-  int r;
+  Walk<MR> walk;
 };
 
-// Every CTA finds its own run: the requests' tiles are summed twice, once for
-// the total and once up to the run's start.
+// Every CTA finds its own run from the requests' lengths: a scan over the
+// requests' tiles, then the thread whose request holds the run's start sets out
+// the walk.  More requests than threads: the tiles are formed twice, once for the
+// total and once up to the start.
 template <int MR, int THREADS>
-__device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem* sm, Walk<MR>* w) {
+__device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR>* w) {
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kW = THREADS / 32;
-  int64_t mine = 0;
+  Span s{0, 0, 0};
+  int64_t mine = 0, per_head = 0;
   bool bad = false;
   for (int r = tid; r < a.B; r += THREADS) {
-    const Span s = span_of(a, r);
+    s = span_of(a, r);
     bad |= s.l < 0;
-    mine += head_tiles<MR>(a, s);
+    per_head = head_tiles<MR>(a, s);
+    mine += per_head;
   }
   if (bad && blockIdx.x == 0 && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_LEN);
-  int64_t sum = mine;
+  mine *= p.kv_heads;
+  int64_t inc = mine;  // up to and with this thread's requests
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  if (lane == 0) sm->part[warp] = sum;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) sm->part[warp] = inc;
   __syncthreads();
-  int64_t total = 0;
-  for (int i = 0; i < kW; ++i) total += sm->part[i];
-  total *= p.kv_heads;
+  int64_t total = 0, before = inc - mine;
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    if (i < warp) before += sm->part[i];
+    total += sm->part[i];
+  }
   const int workers = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
   const int me = blockIdx.x;
-  AttnRecord rec{0, 0, 0, 0, 0};
-  bool any = me < workers;
-  if (any) {
-    const int64_t start = worker_start(total, workers, me);
-    __syncthreads();
+  if (me >= workers) {
+    if (tid == 0) p.record[me] = AttnRecord{0, 0, 0, 0, 0};
+    return false;
+  }
+  const int64_t start = worker_start(total, workers, me);
+  // by the thread with request r, `rem` tiles into it
+  auto set_out = [&](int r, int64_t rem) {
+    Walk<MR> x;
+    x.r = r, x.s = s;
+    x.h = rem < (1 << 30) && per_head < (1 << 30)
+              ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(per_head))
+              : static_cast<int>(rem / per_head);
+    rem -= x.h * per_head;
+    x.m = 0;
+    ItemTiles t = item_tiles<MR>(a, s, 0);
+    while (rem >= t.n) rem -= t.n, t = item_tiles<MR>(a, s, ++x.m);
+    x.off = static_cast<int>(rem);
+    x.left = worker_start(total, workers, me + 1) - start;
+    sm->walk = x;
+    AttnRecord rec{0, 0, 0, 0, 0};
+    const int64_t first = start - x.off;  // the item's first tile
+    if (x.off > 0 && worker_of(total, workers, first) == me - 1)
+      rec = AttnRecord{worker_of(total, workers, first + t.n - 1) - me + 2, t.rows, s.row0, x.h, x.m};
+    p.record[me] = rec;
+  };
+  if (a.B <= THREADS) {
+    if (before <= start && start < before + mine) set_out(tid, start - before);
+  } else {
     int64_t carry = 0;
-    for (int base = 0; base < a.B; base += THREADS) {
+    for (int base = 0; base < a.B && carry <= start; base += THREADS) {
       const int r = base + tid;
-      const int64_t own =
-          (a.B <= THREADS ? mine : r < a.B ? head_tiles<MR>(a, span_of(a, r)) : 0) * p.kv_heads;
-      int64_t inc = own;
+      s = r < a.B ? span_of(a, r) : Span{0, 0, 0};
+      per_head = head_tiles<MR>(a, s);
+      mine = per_head * p.kv_heads;
+      inc = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int64_t o = __shfl_up_sync(~0u, inc, d);
         if (lane >= d) inc += o;
       }
+      __syncthreads();
       if (lane == 31) sm->part[warp] = inc;
       __syncthreads();
-      int64_t before = carry;
+      before = carry + inc - mine;
+#pragma unroll
       for (int i = 0; i < kW; ++i) {
         if (i < warp) before += sm->part[i];
         carry += sm->part[i];
       }
-      if (before + inc - own <= start && start < before + inc)
-        sm->r = r, sm->rem = start - (before + inc - own);
-      __syncthreads();
-      if (carry > start) break;
+      if (before <= start && start < before + mine) set_out(r, start - before);
     }
-    w->r = sm->r;
-    w->s = span_of(a, w->r);
-    int64_t rem = sm->rem;
-    const int64_t per_head = head_tiles<MR>(a, w->s);
-    w->h = static_cast<int>(rem / per_head);
-    rem -= w->h * per_head;
-    w->m = 0;
-    int n = item_tiles<MR>(a, w->s, 0).n;
-    while (rem >= n) rem -= n, n = item_tiles<MR>(a, w->s, ++w->m).n;
-    w->off = static_cast<int>(rem);
-    w->left = worker_start(total, workers, me + 1) - start;
-    const int64_t first = start - w->off;  // the item's first tile
-    if (w->off > 0 && worker_of(total, workers, first) == me - 1)
-      rec = AttnRecord{worker_of(total, workers, first + n - 1) - me + 2,
-                       item_tiles<MR>(a, w->s, w->m).rows, w->s.row0, w->h, w->m};
   }
-  if (tid == 0) p.record[me] = rec;
-  return any;
+  __syncthreads();
+  *w = sm->walk;
+  return true;
 }
 
 // ---------------------------------------------------------------- kernel
@@ -296,11 +320,6 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
   constexpr int kSoftmax = NS * 4, kLoadWarp = kSoftmax, kMmaWarp = kSoftmax + NS;
   bool timed_out = false;
 
-  Walk<MR> walk;
-  const bool any = plan<MR, kThreads>(p, reinterpret_cast<PlanSmem*>(ring), &walk);
-  grid_dep_launch_dependents();
-  if (!any) return;
-  __syncthreads();  // the plan's scratch becomes the ring
   if (tid == 0) {
     for (int i = 0; i < L::kUnits; ++i) {
       mbar_init(smem_addr(&bars->full[i]), TMA ? 1 : 32);
@@ -319,9 +338,16 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(smem_addr(&bars->tmem), kCols);
+  Walk<MR> walk;
+  const bool any = plan<MR, kThreads>(p, reinterpret_cast<PlanSmem<MR>*>(ring), &walk);
+  grid_dep_launch_dependents();
   tmem_fence_before();
-  __syncthreads();
+  __syncthreads();  // and the plan's scratch becomes the ring
   tmem_fence_after();
+  if (!any) {
+    if (warp == kMmaWarp) tmem_free(bars->tmem, kCols);
+    return;
+  }
   const uint32_t tmem = bars->tmem;
   const uint32_t ring_addr = smem_addr(ring), q_addr = smem_addr(qbuf);
   auto full = [&](int u) { return smem_addr(&bars->full[u]); };
@@ -351,7 +377,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           const int t = t0 + lane * p.box;
           int id = 0;
           if (lane < boxes && t < end) {
-            id = __ldg(table + (p.page_shift >= 0 ? t >> p.page_shift : t / a.page));
+            id = __ldg(table + a.by_page.of(t));
             if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
           }
           return id;
@@ -377,7 +403,7 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           const uint32_t dst = ring_addr + u * L::kUnitBytes;
           if (boxes == 1) {
             const int page = __shfl_sync(~0u, id, 0);
-            const int in_page = p.page_shift >= 0 ? t0 & ((1 << p.page_shift) - 1) : t0 % a.page;
+            const int in_page = t0 - a.by_page.of(t0) * a.page;
             if (live > 0 && elect_one()) {
 #pragma unroll
               for (int c = 0; c < L::kChunks; ++c)
@@ -421,9 +447,11 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
             const int t = t0 + k * 32 + lane;
             at[k] = nullptr;
             if (t < g.kv_end) {
-              int id = __ldg(table + t / a.page);
+              const int page = a.by_page.of(t);
+              int id = __ldg(table + page);
               if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
-              at[k] = (val ? a.v : a.k) + id * a.block + (t % a.page) * a.token + g.h * a.head;
+              at[k] = (val ? a.v : a.k) + id * a.block + (t - page * a.page) * a.token +
+                      g.h * a.head;
             }
           }
           if (issued >= L::kUnits) mbar_wait(empty(u), (issued / L::kUnits + 1) & 1, timed_out);
@@ -581,8 +609,8 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       const int i = n.m * MR + st * kRows + wrow + lane;
       const char* src = nullptr;
       if (st * kRows + wrow + lane < n.rows)
-        src = a.q + static_cast<int64_t>(n.row0 + i / a.group) * a.q_row +
-              static_cast<int64_t>(n.h * a.group + i % a.group) * a.q_head;
+        src = a.q + static_cast<int64_t>(n.row0 + a.by_group.of(i)) * a.q_row +
+              static_cast<int64_t>(n.h * a.group + i - a.by_group.of(i) * a.group) * a.q_head;
       constexpr int kPieces = DP / 8;
       if (st * kRows + wrow < n.rows) {
 #pragma unroll 4
@@ -609,12 +637,12 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
       mbar_arrive(smem_addr(&bars->q[st]));
       const bool live = st * kRows < g.rows;         // the stream has rows
       const bool work = st * kRows + wrow < g.rows;  // the warp has rows
-      const int pos = g.seq - g.l + (g.m * MR + st * kRows + row) / a.group;  // of this row
+      const int pos = g.seq - g.l + a.by_group.of(g.m * MR + st * kRows + row);  // of this row
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       // keys that every row of the item sees: [all_lo, all_hi)
-      const int all_hi = g.seq - g.l + g.m * MR / a.group + 1;
+      const int all_hi = g.seq - g.l + a.by_group.of(g.m * MR) + 1;
       const int all_lo = a.window > 0
-          ? max(0, g.seq - g.l + (g.m * MR + g.rows - 1) / a.group - a.window + 1) : 0;
+          ? max(0, g.seq - g.l + a.by_group.of(g.m * MR + g.rows - 1) - a.window + 1) : 0;
       float m = -kInf, l = 0.0f;
 
       if (!live) {
@@ -640,21 +668,30 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           const int at_v = u0 + v_position(g.tile1 - g.tile0, tile - g.tile0);
           mbar_wait(full(at_v % L::kUnits), (turn0 ^ (at_v / L::kUnits)) & 1, timed_out);
           char* unit = ring + at_v % L::kUnits * L::kUnitBytes;
-          for (int at = row; at < L::kUnitBytes / 16; at += 128) {
-            const int t = t0 + (at >> 3) % kTile;
-            if (t >= all_lo && t < all_hi) continue;
-            uint4 v = *reinterpret_cast<const uint4*>(unit + at * 16);
-            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-            bool odd = false;
+          uint32_t big = 0;  // the largest magnitude, NaN above all
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, odd = true;
-              if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, odd = true;
-            }
-            if (odd) {
-              if (t < g.seq) bars->odd = 1;
-              __threadfence_block();
-              *reinterpret_cast<uint4*>(unit + at * 16) = v;
+          for (int at = row; at < L::kUnitBytes / 16; at += 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(unit + at * 16);
+            big = bf16x2_max_nan(big, bf16x2_max_nan(bf16x2_max_nan(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                     bf16x2_max_nan(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+          }
+          if ((big & 0x7f80u) == 0x7f80u || (big & 0x7f800000u) == 0x7f800000u) {
+            for (int at = row; at < L::kUnitBytes / 16; at += 128) {
+              const int t = t0 + (at >> 3) % kTile;
+              if (t >= all_lo && t < all_hi) continue;
+              uint4 v = *reinterpret_cast<const uint4*>(unit + at * 16);
+              uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, odd = true;
+                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, odd = true;
+              }
+              if (odd) {
+                if (t < g.kv_end) bars->odd = 1;  // past it lies what no copy brought
+                __threadfence_block();
+                *reinterpret_cast<uint4*>(unit + at * 16) = v;
+              }
             }
           }
           fence_async_smem();
@@ -743,15 +780,16 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
           const bool valid = st * kRows + row < g.rows;
           const bool odd = *reinterpret_cast<volatile int32_t*>(&bars->odd) != 0;
           const int i = g.m * MR + st * kRows + row;
-          const int head = g.h * a.group + i % a.group;
-          const int64_t orow = g.row0 + i / a.group;
+          const int head = g.h * a.group + i - a.by_group.of(i) * a.group;
+          const int64_t orow = g.row0 + a.by_group.of(i);
           const int slot = 2 * blockIdx.x + (g.begins ? 1 : 0);
           const float inv = g.whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
           const int prow = st * kRows + row;
-#pragma unroll 1
-          for (int k = 0; k < DP; k += 16) {
-            uint32_t x[16];
-            tmem_ld16(o_at + k, x);
+#pragma unroll
+          for (int k0 = 0; k0 < DP; k0 += 64) {
+            uint32_t x[64];
+            tmem_ld32(o_at + k0, x);
+            tmem_ld32(o_at + k0 + 32, x + 32);
             tmem_wait_ld();
             float* o = reinterpret_cast<float*>(x);
             __syncwarp();
@@ -762,31 +800,32 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
                   t = min(all_hi, pos + 1) - 1;
                   continue;
                 }
-                int id = a.table[g.r * a.table_stride + t / a.page];
+                const int page = a.by_page.of(t);
+                int id = a.table[g.r * a.table_stride + page];
                 if (id < 0 || id >= a.num_blocks) id = 0;
                 const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
-                    a.v + id * a.block + (t % a.page) * a.token + g.h * a.head) + k;
+                    a.v + id * a.block + (t - page * a.page) * a.token + g.h * a.head) + k0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (k + e < a.dim && !(fabsf(__bfloat162float(v[e])) < kInf))
+                for (int e = 0; e < 64; ++e)
+                  if (k0 + e < a.dim && !(fabsf(__bfloat162float(v[e])) < kInf))
                     o[e] += __bfloat162float(v[e]);
               }
             }
             if (g.whole) {
-              char* out = a.out + orow * a.o_row + head * a.o_head + k * 2;
+              char* out = a.out + orow * a.o_row + head * a.o_head + k0 * 2;
 #pragma unroll
-              for (int e = 0; e < 16; e += 8) {
+              for (int e = 0; e < 64; e += 8) {
                 uint4 w;
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(o[e + 1] * inv), "f"(o[e] * inv));
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(o[e + 3] * inv), "f"(o[e + 2] * inv));
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.z) : "f"(o[e + 5] * inv), "f"(o[e + 4] * inv));
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.w) : "f"(o[e + 7] * inv), "f"(o[e + 6] * inv));
-                if (k + e < a.dim) *reinterpret_cast<uint4*>(out + e * 2) = w;
+                if (k0 + e < a.dim) *reinterpret_cast<uint4*>(out + e * 2) = w;
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                p.o[(static_cast<int64_t>(slot) * (DP / 4) + (k + e) / 4) * MR + prow] =
+              for (int e = 0; e < 64; e += 4)
+                p.o[(static_cast<int64_t>(slot) * (DP / 4) + (k0 + e) / 4) * MR + prow] =
                     make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
@@ -891,7 +930,8 @@ __global__ __launch_bounds__(kCombineThreads) void attn_combine_kernel(const Mma
         inverse[warp] = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         const int j = r.m * MR + row;
         if (a.lse != nullptr)
-          a.lse[(static_cast<int64_t>(r.row0) + j / a.group) * a.heads + r.h * a.group + j % a.group] =
+          a.lse[(static_cast<int64_t>(r.row0) + a.by_group.of(j)) * a.heads + r.h * a.group + j -
+                a.by_group.of(j) * a.group] =
               l > 0.0f || l != l ? (top + log2f(l)) * kLn2 : -kInf;
       }
     }
@@ -917,8 +957,8 @@ __global__ __launch_bounds__(kCombineThreads) void attn_combine_kernel(const Mma
       uint2 v;
       asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(o.y * inv), "f"(o.x * inv));
       asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(o.w * inv), "f"(o.z * inv));
-      const int64_t orow = static_cast<int64_t>(r.row0) + j / a.group;
-      const int head = r.h * a.group + j % a.group;
+      const int64_t orow = static_cast<int64_t>(r.row0) + a.by_group.of(j);
+      const int head = r.h * a.group + j - a.by_group.of(j) * a.group;
       *reinterpret_cast<uint2*>(a.out + orow * a.o_row + head * a.o_head + q * 8) = v;
     }
   }
