@@ -23,6 +23,8 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+from . import _serve_calls  # noqa: E402  (linked to the library above)
+
 SV_BF16, SV_FP32 = 0, 1
 SV_GREEDY, SV_SAMPLE = 0, 1
 SV_OK = 0
@@ -395,72 +397,21 @@ for _name in ("spec_verify_sample", "spec_verify_slots", "spec_verify_append",
 _DTYPES = {torch.bfloat16: SV_BF16, torch.float32: SV_FP32}
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _issue(fn, device, stream, *args):
-    """Call one entry point on `stream` (None: the device's current one) with
-    the tensors' device current, as the C ABI requires."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
-    else:
-        rc = fn(*args, stream.cuda_stream)
+def _done(rc):
     if rc != SV_OK:
         raise SpecVerifyError(rc)
 
 
-def _new(shape, dtype, device, stream, zero=False):
+def _new(shape, dtype, device, stream):
     """A tensor that the call itself allocates, on the stream that uses it."""
-    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return make(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _expect(name, t, dtype, shape, device):
-    """A contiguous tensor of this dtype and shape on this device (None passes)."""
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {shape}, "
-                         f"got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _rows_of_heads(name, t, dtype, device):
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be [rows, heads, head_dim] with a contiguous last dimension")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _caches(key_cache, value_cache, kv_heads, head_dim, dtype, device):
-    """The strides that both caches share."""
-    for name, c in (("key_cache", key_cache), ("value_cache", value_cache)):
-        if c.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {c.dtype}")
-        if c.dim() != 4 or (head_dim > 1 and c.stride(3) != 1):
-            raise ValueError(f"{name} must be [num_blocks, page_size, kv_heads, head_dim] with a "
-                             "contiguous last dimension")
-        if c.device != device:
-            raise ValueError(f"{name} is on {c.device}, expected {device}")
-    if key_cache.shape != value_cache.shape or key_cache.stride() != value_cache.stride():
-        raise ValueError("key_cache and value_cache must have the same shape and strides")
-    if kv_heads is not None and key_cache.shape[2] != kv_heads:
-        raise ValueError(f"the caches hold {key_cache.shape[2]} heads, expected {kv_heads}")
-    if key_cache.shape[3] != head_dim:
-        raise ValueError(f"the caches' head_dim is {key_cache.shape[3]}, expected {head_dim}")
-    return key_cache.stride()
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def spec_verify_sample(logits, uniforms, *, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -471,27 +422,12 @@ def spec_verify_sample(logits, uniforms, *, temperature=None, top_k=None, top_p=
     and min_p, each a [N] tensor or None (1, off, off, off); temperature 0 is
     the argmax.  Returns (tokens int32 [N], probs float32 [N] or None: the
     token's probability in the kept set)."""
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be [N, V] with contiguous rows")
-    if logits.dtype not in _DTYPES:
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    (N, V), dev = logits.shape, logits.device
-    _expect("uniforms", uniforms, torch.float32, (N,), dev)
-    _expect("temperature", temperature, torch.float32, (N,), dev)
-    _expect("top_k", top_k, torch.int32, (N,), dev)
-    _expect("top_p", top_p, torch.float32, (N,), dev)
-    _expect("min_p", min_p, torch.float32, (N,), dev)
-    _expect("out_tokens", out_tokens, torch.int32, (N,), dev)
-    _expect("out_probs", out_probs, torch.float32, (N,), dev)
-    _expect("dev_error", dev_error, torch.int32, (1,), dev)
     if out_tokens is None:
-        out_tokens = _new(N, torch.int32, dev, stream)
+        out_tokens = _new(logits.shape[0], torch.int32, logits.device, stream)
     if out_probs is None and want_probs:
-        out_probs = _new(N, torch.float32, dev, stream)
-    _issue(_lib.spec_verify_sample, dev, stream, logits.data_ptr(),
-           max(logits.stride(0), V) if N < 2 else logits.stride(0), N, V, _DTYPES[logits.dtype],
-           _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p), uniforms.data_ptr(),
-           out_tokens.data_ptr(), _addr(out_probs), _addr(dev_error))
+        out_probs = _new(logits.shape[0], torch.float32, logits.device, stream)
+    _done(_serve_calls.sample(logits, uniforms, temperature, top_k, top_p, min_p, out_tokens,
+                              out_probs, dev_error, _handle(stream)))
     return out_tokens, out_probs
 
 
@@ -518,28 +454,11 @@ def spec_verify_slots(context_lens, verify_lens, block_table, held, free_list, f
     sums of verify_lens [B + 1], sequence lengths [B], and for ``n_rows`` rows
     (at least the sum of verify_lens; the length of ``slots`` if given) the
     positions int32 and slots int64."""
-    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [B, width] with contiguous rows")
-    (B, width), dev = block_table.shape, block_table.device
-    if block_table.dtype != torch.int32:
-        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
     if n_rows is None:
         if slots is None:
             raise ValueError("n_rows is needed where slots is not given")
         n_rows = slots.numel()
-    i32 = torch.int32
-    _expect("context_lens", context_lens, i32, (B,), dev)
-    _expect("verify_lens", verify_lens, i32, (B,), dev)
-    _expect("held", held, i32, (B,), dev)
-    _expect("free_list", free_list, i32, (free_list.numel(),), dev)
-    _expect("free_count", free_count, i32, (1,), dev)
-    _expect("row_offsets", row_offsets, i32, (B + 1,), dev)
-    _expect("seq_lens", seq_lens, i32, (B,), dev)
-    _expect("positions", positions, i32, (n_rows,), dev)
-    _expect("slots", slots, torch.int64, (n_rows,), dev)
-    _expect("held_out", held_out, i32, (B,), dev)
-    _expect("free_count_out", free_count_out, i32, (1,), dev)
-    _expect("dev_error", dev_error, i32, (1,), dev)
+    B, dev, i32 = block_table.shape[0], block_table.device, torch.int32
     if row_offsets is None:
         row_offsets = _new(B + 1, i32, dev, stream)
     if seq_lens is None:
@@ -552,12 +471,9 @@ def spec_verify_slots(context_lens, verify_lens, block_table, held, free_list, f
         held_out = _new(B, i32, dev, stream)
     if free_count_out is None:
         free_count_out = _new(1, i32, dev, stream)
-    _issue(_lib.spec_verify_slots, dev, stream, context_lens.data_ptr(), verify_lens.data_ptr(),
-           B, page_size, block_table.data_ptr(),
-           max(block_table.stride(0), width) if B < 2 else block_table.stride(0), width,
-           held.data_ptr(), free_list.data_ptr(), free_list.numel(), free_count.data_ptr(), n_rows,
-           row_offsets.data_ptr(), seq_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(),
-           held_out.data_ptr(), free_count_out.data_ptr(), _addr(dev_error))
+    _done(_serve_calls.slots(context_lens, verify_lens, block_table, held, free_list, free_count,
+                             page_size, n_rows, row_offsets, seq_lens, positions, slots, held_out,
+                             free_count_out, dev_error, _handle(stream)))
     return SlotOutputs(row_offsets, seq_lens, positions, slots, held_out, free_count_out)
 
 
@@ -567,21 +483,8 @@ def spec_verify_append(key, value, slots, key_cache, value_cache, *, dev_error=N
     caches [num_blocks, page_size, kv_heads, head_dim] (any strides; a cache
     laid out [num_blocks, kv_heads, page_size, head_dim] is passed transposed).
     Negative slots are skipped."""
-    dev, dtype = key_cache.device, key_cache.dtype
-    if dtype not in _DTYPES:
-        raise TypeError(f"the caches must be bfloat16 or float32, got {dtype}")
-    _rows_of_heads("key", key, dtype, dev)
-    _rows_of_heads("value", value, dtype, dev)
-    if key.shape != value.shape:
-        raise ValueError("key and value must have the same shape")
-    N, H, D = key.shape
-    sb, st, sh, _ = _caches(key_cache, value_cache, H, D, dtype, dev)
-    _expect("slots", slots, torch.int64, (N,), dev)
-    _expect("dev_error", dev_error, torch.int32, (1,), dev)
-    _issue(_lib.spec_verify_append, dev, stream, key.data_ptr(), value.data_ptr(), key.stride(0),
-           key.stride(1), value.stride(0), value.stride(1), slots.data_ptr(), N, H, D,
-           key_cache.data_ptr(), value_cache.data_ptr(), sb, st, sh, key_cache.shape[0],
-           key_cache.shape[1], _DTYPES[dtype], _addr(dev_error))
+    _done(_serve_calls.append(key, value, slots, key_cache, value_cache, dev_error,
+                              _handle(stream)))
 
 
 def spec_verify_attention_workspace_size(n_rows, heads, head_dim, dtype=torch.bfloat16) -> int:
@@ -604,42 +507,16 @@ def spec_verify_attention(query, key_cache, value_cache, block_table, seq_lens, 
     ``window`` > 0 keeps the last window keys of each row; ``scale`` defaults to
     head_dim ** -0.5; ``max_len`` is a host upper bound of the new tokens of a
     request.  Returns (out, lse or None)."""
-    dev, dtype = query.device, query.dtype
-    if dtype not in _DTYPES:
-        raise TypeError(f"query must be bfloat16 or float32, got {dtype}")
-    _rows_of_heads("query", query, dtype, dev)
-    N, H, D = query.shape
-    sb, st, sh, _ = _caches(key_cache, value_cache, None, D, dtype, dev)
-    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [B, width] with contiguous rows")
-    if block_table.dtype != torch.int32:
-        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
-    if block_table.device != dev:
-        raise ValueError(f"block_table is on {block_table.device}, expected {dev}")
-    B, width = block_table.shape
-    _expect("seq_lens", seq_lens, torch.int32, (B,), dev)
-    _expect("row_offsets", row_offsets, torch.int32, (B + 1,), dev)
-    _expect("lse", lse, torch.float32, (N, H), dev)
-    _expect("dev_error", dev_error, torch.int32, (1,), dev)
     if out is None:
-        out = _new((N, H, D), dtype, dev, stream)
-    else:
-        _rows_of_heads("out", out, dtype, dev)
-        if out.shape != query.shape:
-            raise ValueError("out must have the query's shape")
+        out = _new(query.shape, query.dtype, query.device, stream)
     if lse is None and want_lse:
-        lse = _new((N, H), torch.float32, dev, stream)
+        lse = _new(query.shape[:2], torch.float32, query.device, stream)
     if workspace is None:
-        workspace = _new(spec_verify_attention_workspace_size(N, H, D, dtype), torch.uint8, dev,
-                         stream)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
-    _issue(_lib.spec_verify_attention, dev, stream, query.data_ptr(), query.stride(0),
-           query.stride(1), key_cache.data_ptr(), value_cache.data_ptr(), sb, st, sh,
-           block_table.data_ptr(), max(block_table.stride(0), width) if B < 2 else
-           block_table.stride(0), width, seq_lens.data_ptr(), row_offsets.data_ptr(), B, N,
-           max_len, H, key_cache.shape[2], D, key_cache.shape[0], key_cache.shape[1],
-           _DTYPES[dtype], D ** -0.5 if scale is None else scale, window, out.data_ptr(),
-           out.stride(0), out.stride(1), _addr(lse), _addr(dev_error), workspace.data_ptr(),
-           workspace.numel() * workspace.element_size())
+        if query.dtype not in _DTYPES:
+            raise TypeError(f"query must be bfloat16 or float32, got {query.dtype}")
+        workspace = _new(spec_verify_attention_workspace_size(*query.shape, query.dtype),
+                         torch.uint8, query.device, stream)
+    _done(_serve_calls.attention(query, key_cache, value_cache, block_table, seq_lens, row_offsets,
+                                 max_len, query.shape[-1] ** -0.5 if scale is None else scale,
+                                 window, out, lse, dev_error, workspace, _handle(stream)))
     return out, lse

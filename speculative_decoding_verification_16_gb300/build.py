@@ -1,4 +1,6 @@
-"""Build step of the C-ABI library ``libspecverify.so`` (sm_103a).
+"""Build step of the C-ABI library ``libspecverify.so`` (sm_103a) and of
+``_serve_calls.so``, the serving operators' argument marshalling for Python
+(host code over torch's headers, linked to the library).
 
 One translation unit each for the verify step, its vocabulary-sharded form,
 slot maps and cache writes, sampling, and paged attention; one ``-gencode``,
@@ -17,6 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libspecverify.so")
+CALLS = os.path.join(HERE, "_serve_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "serve_calls.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "sv_shard.cu", "sv_slots.cu",
                                            "sv_sample.cu", "sv_attention.cu")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
@@ -35,21 +39,49 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libspecverify.so")
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libspecverify.so if needed; returns its path."""
-    if not force and os.path.exists(LIB):
-        t = os.path.getmtime(LIB)
-        if all(os.path.getmtime(f) <= t for f in _deps()):
-            return LIB
-    cmd = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "--threads", "0",
-           "-Xcompiler", "-fPIC", "-Xptxas", "-v" if verbose else "-O3",
-           "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", LIB + ".tmp", "-lcudart"]
+def _stale(target, deps):
+    if not os.path.exists(target):
+        return True
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(f) > t for f in deps)
+
+
+def _run(tool, cmd, verbose):
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+        raise RuntimeError(f"{tool} failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
     if verbose:
         print(res.stdout + res.stderr)
-    os.replace(LIB + ".tmp", LIB)
+
+
+def _build_calls(verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    inc = [os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(root, "lib")
+    _run("g++", ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
+                 *[x for i in inc for x in ("-isystem", i)],
+                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                 CALLS_SOURCE, "-o", CALLS + ".tmp", LIB, f"-L{lib}", "-ltorch_python", "-ltorch",
+                 "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,$ORIGIN:{lib}"], verbose)
+    os.replace(CALLS + ".tmp", CALLS)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile what is out of date; returns the path of libspecverify.so."""
+    if force or _stale(LIB, _deps()):
+        _run("nvcc", [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "--threads", "0",
+                      "-Xcompiler", "-fPIC", "-Xptxas", "-v" if verbose else "-O3",
+                      "-Xlinker", "-soname=libspecverify.so",
+                      "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", LIB + ".tmp", "-lcudart"], verbose)
+        os.replace(LIB + ".tmp", LIB)
+    if force or _stale(CALLS, [CALLS_SOURCE, LIB]):
+        _build_calls(verbose)
     return LIB
 
 

@@ -852,16 +852,17 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
 //
 // Joins the partials of the items that were cut.  Every block finds all of them
 // from the workers' records and takes four rows at a time: the parts' weights
-// 2^(m c - max) go to shared memory, then a thread sums four columns of a row
-// over the parts, in worker order.  Bound by the latency of two rounds of loads,
+// 2^(m c - max) go to shared memory, then GROUPS threads sum four columns of a row,
+// each over every GROUPS-th part, in worker order.  Bound by the latency of two rounds of loads,
 // and by the partials' bytes (from L2) where there are many.
-constexpr int kCombineThreads = 128;
 constexpr int kCombineRows = 4;
 
-template <int MR, int DP>
-__global__ __launch_bounds__(kCombineThreads) void attn_combine_kernel(const MmaArgs p, int workers) {
+template <int MR, int DP, int GROUPS>
+__global__ __launch_bounds__(GROUPS * 128) void attn_combine_kernel(const MmaArgs p, int workers) {
+  constexpr int kCombineThreads = GROUPS * 128, kCombineGroups = GROUPS;
   __shared__ AttnRecord item[kMaxWorkers];
   __shared__ int32_t second[kMaxWorkers];  // the item's second worker
+  __shared__ float4 sums[GROUPS > 1 ? GROUPS - 1 : 1][128];
   __shared__ float weight[kCombineRows][kMaxWorkers], inverse[kCombineRows];
   __shared__ int32_t found[(kMaxWorkers + kCombineThreads - 1) / kCombineThreads * (kCombineThreads / 32)];
   const AttnArgs& a = p.a;
@@ -901,17 +902,18 @@ __global__ __launch_bounds__(kCombineThreads) void attn_combine_kernel(const Mma
     const int rows = r.rows;
     if (row0 >= rows) continue;
     auto slot = [&](int i) { return static_cast<int64_t>(2 * (w0 + i) + (i == 0 ? 1 : 0)); };
-    // thread: row row0 + tid % 4, columns [4 q, 4 q + 4); the first parts' loads go
-    // out before the weights are known
-    const int sub = tid % kCombineRows, q = tid / kCombineRows, mine_row = row0 + sub;
+    // thread: row row0 + tid % 4, columns [4 q, 4 q + 4), parts group, group + 4, ..;
+    // the first parts' loads go out before the weights are known
+    const int sub = tid % kCombineRows, q = tid / kCombineRows % 32, group = tid / 128,
+              mine_row = row0 + sub;
     const bool on = mine_row < rows && q * 4 < a.dim;
     auto load = [&](int i) { return p.o[(slot(i) * (DP / 4) + q) * MR + mine_row]; };
     float4 x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (on && j < r.parts) x[j] = load(j);
+      if (on && group + j * kCombineGroups < r.parts) x[j] = load(group + j * kCombineGroups);
     __syncthreads();  // the weights of the task before are done with
-    if (row0 + warp < rows) {  // warp j: the weights of row row0 + j
+    if (warp < kCombineRows && row0 + warp < rows) {  // warp j: the weights of row row0 + j
       const int row = row0 + warp;
       float top = -kInf, l = 0.0f;
       for (int i = lane; i < r.parts; i += 32) top = fmaxf(top, p.ml[slot(i) * MR + row].x);
@@ -936,21 +938,30 @@ __global__ __launch_bounds__(kCombineThreads) void attn_combine_kernel(const Mma
       }
     }
     __syncthreads();
-    if (on) {
-      float4 o = make_float4(0, 0, 0, 0);
-      for (int i = 0; i < r.parts; i += 8) {
-        if (i > 0) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (i + j < r.parts) x[j] = load(i + j);
-        }
+    float4 o = make_float4(0, 0, 0, 0);
+    for (int i = group; i < r.parts; i += 8 * kCombineGroups) {
+      if (i > group) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (i + j < r.parts) {
-            const float f = weight[sub][i + j];
-            o.x = fmaf(x[j].x, f, o.x), o.y = fmaf(x[j].y, f, o.y);
-            o.z = fmaf(x[j].z, f, o.z), o.w = fmaf(x[j].w, f, o.w);
-          }
+          if (on && i + j * kCombineGroups < r.parts) x[j] = load(i + j * kCombineGroups);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (on && i + j * kCombineGroups < r.parts) {
+          const float f = weight[sub][i + j * kCombineGroups];
+          o.x = fmaf(x[j].x, f, o.x), o.y = fmaf(x[j].y, f, o.y);
+          o.z = fmaf(x[j].z, f, o.z), o.w = fmaf(x[j].w, f, o.w);
+        }
+    }
+    if (GROUPS > 1) {
+      if (group > 0) sums[group - 1][tid % 128] = o;
+      __syncthreads();
+    }
+    if (on && group == 0) {
+#pragma unroll
+      for (int j = 0; j < kCombineGroups - 1; ++j) {
+        const float4 y = sums[j][tid];
+        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
       }
       const float inv = inverse[sub];
       const int j = r.m * MR + mine_row;
