@@ -17,20 +17,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_huge_valf();
 
-// Division of 0 <= n < 2^31 by a fixed d: n / d = (mulhi(n, mul) + n) >> shift with
-// mul = 2^32 (2^shift - d) / d + 1, 2^shift >= d (Granlund and Montgomery 1994).
-struct FastDiv {
-  uint32_t mul, shift;
-  static FastDiv by(uint32_t d) {
-    uint32_t s = 0;
-    while ((uint64_t{1} << s) < d) ++s;
-    return FastDiv{static_cast<uint32_t>((((uint64_t{1} << s) - d) << 32) / d + 1), s};
-  }
-  __device__ __forceinline__ int of(int n) const {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
-  }
-};
-
 struct AttnArgs {
   const char* q;
   int64_t q_row, q_head;  // bytes
@@ -222,7 +208,7 @@ int launch_mma(const MmaArgs& p, int grid, int64_t items, int64_t joins, const C
   int rc = p.box > 0
                ? launch(attn_mma_kernel<NS, DP, true>, dim3(grid), threads, smem, 1, false, st, p, km, vm)
                : launch(attn_mma_kernel<NS, DP, false>, dim3(grid), threads, smem, 1, false, st, p, km, vm);
-  if (rc != SV_OK || grid == 1) return rc;  // one worker cuts no item
+  if (rc != SV_OK || grid == 1 || p.whole) return rc;  // no item is cut
   Device d;
   rc = device(&d);
   if (rc != SV_OK) return rc;
@@ -244,7 +230,7 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
   if (rc != SV_OK) return rc;
   const int dp = a.dim <= 64 ? 64 : 128;
   char* ws = static_cast<char*>(workspace);
-  MmaArgs p{a, kv_heads, 0, reinterpret_cast<AttnRecord*>(ws),
+  MmaArgs p{a, kv_heads, 0, false, reinterpret_cast<AttnRecord*>(ws),
             reinterpret_cast<float2*>(ws + kRecordBytes),
             reinterpret_cast<float4*>(ws + kRecordBytes + kMlBytes)};
   // whole page pieces by tensor copies where pages hold a number of them and
@@ -262,7 +248,10 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
   const int64_t rows = std::min<int64_t>(a.max_len, a.n_rows) * a.group;
   const int ns = rows > kRows ? 2 : 1;
   const int64_t keys = static_cast<int64_t>(a.table_width) * a.page;
-  const int64_t tiles = (rows + ns * kRows - 1) / (ns * kRows) * ((keys + kTile - 1) / kTile) *
+  // items of at most four tiles are not cut: the parts' latency and the second
+  // launch would cost what they save
+  p.whole = keys <= 4 * kTile;
+  const int64_t tiles = (rows + ns * kRows - 1) / (ns * kRows) * (p.whole ? 1 : (keys + kTile - 1) / kTile) *
                         a.B * kv_heads;
   const int64_t most = ns == 1 ? std::min(2 * d.sms, kMaxWorkers) : std::min(d.sms, kMaxWorkers / 2);
   const int grid = static_cast<int>(std::min(most, tiles));

@@ -61,6 +61,7 @@ struct AttnRecord {  // of a worker whose run is the second in an item
 struct MmaArgs {
   AttnArgs a;
   int32_t kv_heads, box;  // box: tokens of a tensor copy; 0: copies of single rows
+  bool whole;             // items are not cut
   AttnRecord* record;     // [kMaxWorkers]
   float2* ml;             // [2 * kMaxWorkers][rows]: m c and l of the partials
   float4* o;              // [2 * kMaxWorkers][DP / 4][rows]
@@ -85,11 +86,13 @@ struct Segment {  // consecutive tiles of one item
 };
 
 struct ItemTiles {
-  int lo, n, rows, kv_end;
+  int lo, tiles, rows, kv_end;
+  int n;  // its share of the work: the tiles, or 1 where items are not cut
 };
 
 template <int MR>
-__device__ __forceinline__ ItemTiles item_tiles(const AttnArgs& a, const Span& s, int m) {
+__device__ __forceinline__ ItemTiles item_tiles(const MmaArgs& p, const Span& s, int m) {
+  const AttnArgs& a = p.a;
   ItemTiles t;
   const int all = s.l * a.group;
   t.rows = min(MR, all - m * MR);
@@ -97,15 +100,16 @@ __device__ __forceinline__ ItemTiles item_tiles(const AttnArgs& a, const Span& s
   t.kv_end = max(0, s.seq - s.l + j1 + 1);
   const int kv_lo = a.window > 0 ? max(0, s.seq - s.l + j0 - a.window + 1) : 0;
   t.lo = kv_lo / kTile;
-  t.n = max(1, (t.kv_end + kTile - 1) / kTile - t.lo);
+  t.tiles = max(1, (t.kv_end + kTile - 1) / kTile - t.lo);
+  t.n = p.whole ? 1 : t.tiles;
   return t;
 }
 
 template <int MR>
-__device__ __forceinline__ int64_t head_tiles(const AttnArgs& a, const Span& s) {
+__device__ __forceinline__ int64_t head_tiles(const MmaArgs& p, const Span& s) {
   int64_t n = 0;
   if (s.l > 0)
-    for (int m = 0; m * MR < s.l * a.group; ++m) n += item_tiles<MR>(a, s, m).n;
+    for (int m = 0; m * MR < s.l * p.a.group; ++m) n += item_tiles<MR>(p, s, m).n;
   return n;
 }
 
@@ -130,10 +134,10 @@ struct Walk {  // a worker's segments in order
 
   __device__ __forceinline__ bool next(const MmaArgs& p, Segment* g) {
     if (left <= 0) return false;
-    const ItemTiles t = item_tiles<MR>(p.a, s, m);
+    const ItemTiles t = item_tiles<MR>(p, s, m);
     const int take = static_cast<int>(min(left, static_cast<int64_t>(t.n - off)));
     g->r = r, g->h = h, g->m = m, g->row0 = s.row0, g->l = s.l, g->seq = s.seq;
-    g->tile0 = t.lo + off, g->tile1 = t.lo + off + take;
+    g->tile0 = t.lo + off, g->tile1 = t.lo + (p.whole ? t.tiles : off + take);
     g->rows = t.rows, g->kv_end = t.kv_end;
     g->begins = off == 0, g->whole = off == 0 && take == t.n;
     left -= take;
@@ -173,7 +177,7 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
   for (int r = tid; r < a.B; r += THREADS) {
     s = span_of(a, r);
     bad |= s.l < 0;
-    per_head = head_tiles<MR>(a, s);
+    per_head = head_tiles<MR>(p, s);
     mine += per_head;
   }
   if (bad && blockIdx.x == 0 && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_LEN);
@@ -200,6 +204,7 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
   }
   const int64_t start = worker_start(total, workers, me);
   // by the thread with request r, `rem` tiles into it
+  int item = -1;  // its item's tiles, in that thread
   auto set_out = [&](int r, int64_t rem) {
     Walk<MR> x;
     x.r = r, x.s = s;
@@ -208,16 +213,12 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
               : static_cast<int>(rem / per_head);
     rem -= x.h * per_head;
     x.m = 0;
-    ItemTiles t = item_tiles<MR>(a, s, 0);
-    while (rem >= t.n) rem -= t.n, t = item_tiles<MR>(a, s, ++x.m);
+    ItemTiles t = item_tiles<MR>(p, s, 0);
+    while (rem >= t.n) rem -= t.n, t = item_tiles<MR>(p, s, ++x.m);
     x.off = static_cast<int>(rem);
     x.left = worker_start(total, workers, me + 1) - start;
     sm->walk = x;
-    AttnRecord rec{0, 0, 0, 0, 0};
-    const int64_t first = start - x.off;  // the item's first tile
-    if (x.off > 0 && worker_of(total, workers, first) == me - 1)
-      rec = AttnRecord{worker_of(total, workers, first + t.n - 1) - me + 2, t.rows, s.row0, x.h, x.m};
-    p.record[me] = rec;
+    item = t.n;
   };
   if (a.B <= THREADS) {
     if (before <= start && start < before + mine) set_out(tid, start - before);
@@ -226,7 +227,7 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
     for (int base = 0; base < a.B && carry <= start; base += THREADS) {
       const int r = base + tid;
       s = r < a.B ? span_of(a, r) : Span{0, 0, 0};
-      per_head = head_tiles<MR>(a, s);
+      per_head = head_tiles<MR>(p, s);
       mine = per_head * p.kv_heads;
       inc = mine;
 #pragma unroll
@@ -248,6 +249,14 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
   }
   __syncthreads();
   *w = sm->walk;
+  if (item >= 0) {  // the record, while the others go on
+    AttnRecord rec{0, 0, 0, 0, 0};
+    const int64_t first = start - w->off;  // the item's first tile
+    if (w->off > 0 && worker_of(total, workers, first) == me - 1)
+      rec = AttnRecord{worker_of(total, workers, first + item - 1) - me + 2,
+                       item_tiles<MR>(p, w->s, w->m).rows, w->s.row0, w->h, w->m};
+    p.record[me] = rec;
+  }
   return true;
 }
 

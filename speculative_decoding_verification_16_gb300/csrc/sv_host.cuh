@@ -16,6 +16,20 @@ inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintpt
 // A device pointer that may be NULL but, if given, is aligned.
 inline bool null_or_aligned(const void* p, size_t a) { return p == nullptr || aligned_to(p, a); }
 
+// Division of 0 <= n < 2^31 by a fixed d: n / d = (mulhi(n, mul) + n) >> shift with
+// mul = 2^32 (2^shift - d) / d + 1, 2^shift >= d (Granlund and Montgomery 1994).
+struct FastDiv {
+  uint32_t mul, shift;
+  static FastDiv by(uint32_t d) {
+    uint32_t s = 0;
+    while ((uint64_t{1} << s) < d) ++s;
+    return FastDiv{static_cast<uint32_t>((((uint64_t{1} << s) - d) << 32) / d + 1), s};
+  }
+  __device__ __forceinline__ int of(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
+
 struct Device {
   int sms = 0;
   int max_smem = 0;

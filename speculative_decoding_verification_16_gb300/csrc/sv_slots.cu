@@ -86,6 +86,7 @@ struct SlotsArgs {
   int32_t *row_offsets, *seq_lens, *positions;
   int64_t* slots;
   int32_t *held_out, *free_count_out, *dev_error;
+  FastDiv by_page;
 };
 
 struct Request {
@@ -99,11 +100,16 @@ __device__ __forceinline__ Request load_request(const SlotsArgs& a, int r) {
   q.fresh = a.fresh[r];
   q.held = a.held[r];
   const bool rows_ok = q.fresh >= 0 && q.fresh <= a.n_rows;
-  const int64_t seq = static_cast<int64_t>(q.ctx) + q.fresh;
-  const int64_t need = (seq + a.page - 1) / a.page;
-  q.ok = rows_ok && q.ctx >= 0 && q.held >= 0 && q.held <= a.width && need <= a.width;
   if (!rows_ok) q.fresh = 0;
-  q.need = q.ok ? static_cast<int32_t>(need) : q.held;
+  const uint32_t seq = static_cast<uint32_t>(q.ctx) + static_cast<uint32_t>(q.fresh);
+  q.ok = rows_ok && q.ctx >= 0 && seq <= INT32_MAX && q.held >= 0 && q.held <= a.width;
+  q.need = q.held;
+  if (q.ok) {
+    const int pages = a.by_page.of(static_cast<int>(seq));
+    const int need = pages + (static_cast<int>(seq) > pages * a.page ? 1 : 0);
+    if (need <= a.width) q.need = need;
+    else q.ok = false;
+  }
   return q;
 }
 
@@ -123,6 +129,8 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
   int32_t* offs = sm;              // [B + 1] rows before request r
   int32_t* give = offs + a.B + 1;  // [B + 1] pages given back before r
   int32_t* take = give + a.B + 1;  // [B + 1] pages taken before r
+  int32_t* ctxs = take + a.B + 1;  // [B] context
+  int32_t* keep = ctxs + a.B;      // [B] pages held before the call, -1: left out
   __shared__ int64_t part0[kSlotWarps];
   __shared__ int32_t part1[kSlotWarps], part2[kSlotWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -143,6 +151,7 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
       s1 = max(q.held - q.need, 0);
       s2 = max(q.need - q.held, 0);
       if (!q.ok) err |= SV_DEVERR_LEN;
+      ctxs[r] = q.ctx, keep[r] = q.ok ? q.held : -1;
       if (first)
         a.seq_lens[r] = static_cast<int32_t>(
             min(static_cast<int64_t>(q.ctx) + q.fresh, static_cast<int64_t>(INT32_MAX)));
@@ -181,7 +190,8 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
   // the i-th page given back in this call
   auto returned_page = [&](int32_t i) {
     const int r = last_at_or_below(give, a.B, i);
-    return a.table[r * a.table_stride + load_request(a, r).need + (i - give[r])];
+    const int32_t need = keep[r] - (give[r + 1] - give[r]);
+    return a.table[r * a.table_stride + need + (i - give[r])];
   };
   // the k-th page taken: k-th from the top of the list after the returns
   auto taken_page = [&](int32_t k) {
@@ -192,10 +202,11 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
   if (first) {
     for (int r = tid; r <= a.B; r += kSlotThreads) a.row_offsets[r] = offs[r];
     for (int r = tid; r < a.B; r += kSlotThreads) {
-      const Request q = load_request(a, r);
-      const bool served = take[r + 1] <= avail || take[r + 1] == take[r];
+      const int32_t taken = take[r + 1] - take[r];
+      const bool served = take[r + 1] <= avail || taken == 0;
       if (!served) err |= SV_DEVERR_BLOCKS;
-      a.held_out[r] = q.ok && served ? q.need : q.held;
+      a.held_out[r] = keep[r] < 0 ? a.held[r]
+                                  : keep[r] + (served ? taken : 0) - (give[r + 1] - give[r]);
     }
     if (tid == 0) {
       const int r = last_at_or_below(take, a.B + 1, static_cast<int32_t>(
@@ -211,7 +222,7 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
   for (int64_t k = start; k < take[a.B]; k += step) {
     const int r = last_at_or_below(take, a.B, static_cast<int32_t>(k));
     if (take[r + 1] > avail) continue;  // not served
-    a.table[r * a.table_stride + a.held[r] + (k - take[r])] =
+    a.table[r * a.table_stride + keep[r] + (k - take[r])] =
         taken_page(static_cast<int32_t>(k));
   }
   for (int64_t i = start; i < a.n_rows; i += step) {
@@ -219,15 +230,14 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
     int64_t slot = -1;
     if (i < offs[a.B]) {
       const int r = last_at_or_below(offs, a.B, static_cast<int32_t>(i));
-      const Request q = load_request(a, r);
-      if (q.ok) {
-        pos = q.ctx + static_cast<int32_t>(i) - offs[r];
-        const int32_t col = pos / a.page;
+      if (keep[r] >= 0) {
+        pos = ctxs[r] + static_cast<int32_t>(i) - offs[r];
+        const int32_t col = a.by_page.of(pos);
         int32_t id = -1;
-        if (col < q.held)
+        if (col < keep[r])
           id = a.table[r * a.table_stride + col];
         else if (take[r + 1] <= avail)
-          id = taken_page(take[r] + col - q.held);
+          id = taken_page(take[r] + col - keep[r]);
         if (id >= 0) slot = static_cast<int64_t>(id) * a.page + (pos - col * a.page);
       }
     }
@@ -339,11 +349,12 @@ int spec_verify_slots(const int32_t* context_lens, const int32_t* verify_lens, i
   const sv::serve::SlotsArgs a{context_lens, verify_lens, B, page_size, block_table, table_stride,
                                width, held, free_list, free_cap, free_count, n_rows,
                                out_row_offsets, out_seq_lens, out_positions, out_slots, out_held,
-                               out_free_count, dev_error};
+                               out_free_count, dev_error,
+                               sv::serve::FastDiv::by(static_cast<uint32_t>(page_size))};
   const int grid = std::max(1, std::min(d.sms, (n_rows + sv::serve::kSlotRowsPerCta - 1) /
                                                    sv::serve::kSlotRowsPerCta));
   return sv::serve::launch(sv::serve::slots_kernel, dim3(grid), sv::serve::kSlotThreads,
-                           3 * (B + 1) * 4, 1, false, static_cast<cudaStream_t>(stream), a);
+                           (5 * B + 3) * 4, 1, false, static_cast<cudaStream_t>(stream), a);
 }
 
 int spec_verify_append(const void* key, const void* value, int64_t k_row_stride,
