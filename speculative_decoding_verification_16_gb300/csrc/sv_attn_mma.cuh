@@ -51,6 +51,7 @@ namespace serve {
 constexpr int kRows = 128;        // query rows of a stream
 constexpr int kTile = 64;         // keys of a tile
 constexpr int kMaxWorkers = 320;  // partials are laid out for this many
+constexpr int kMinRun = 3;        // least tiles of a worker's run
 constexpr float kRescale = 8.0f;  // log2 of how far P may exceed 1 before O is rescaled
 
 struct AttnRecord {  // of a worker whose run is the second in an item
@@ -196,7 +197,11 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
     if (i < warp) before += sm->part[i];
     total += sm->part[i];
   }
-  const int workers = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  // runs of at least three tiles: shorter ones cost more in partials and their join
+  // than they save (one request's verify step 17.8 us at one, 16.3 at three, 18.0 at
+  // four; 54 single tokens over up to 1,216 keys 24.8, 18.5, 19.1)
+  const int workers = static_cast<int>(
+      min(static_cast<int64_t>(gridDim.x), p.whole ? total : (total + kMinRun - 1) / kMinRun));
   const int me = blockIdx.x;
   if (me >= workers) {
     if (tid == 0) p.record[me] = AttnRecord{0, 0, 0, 0, 0};
@@ -370,8 +375,9 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
     if constexpr (TMA) {
       // NS = 1: one warp copies K and V in the ring's order; NS = 2: one the Ks,
       // one the Vs (one for both took 1,000 cycles a unit, of which a pair of
-      // tiles has two in some 1,300).  The page ids are loaded one unit ahead,
-      // lane b those of the unit's box b; one lane issues the copies.
+      // tiles has two in some 1,300).  A lane holds the page id of one box, so a
+      // load brings those of 32 / boxes tiles; the next chunk's is under way while
+      // one is used, and Vs may still be in the one before.
       const int side = __shfl_sync(~0u, warp - kLoadWarp, 0);
       const int boxes = kTile / p.box;
       const uint32_t bytes = static_cast<uint32_t>(p.box) * L::kChunks * 128;
@@ -382,36 +388,38 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
         const int tile0 = __shfl_sync(~0u, g.tile0, 0), end = __shfl_sync(~0u, g.kv_end, 0),
                   head = __shfl_sync(~0u, g.h, 0);
         const int32_t* table = a.table + g.r * a.table_stride;
-        auto load_id = [&](int t0) {
-          const int t = t0 + lane * p.box;
+        const int shift = __ffs(32 / boxes) - 1, per = 1 << shift;  // tiles of a chunk
+        auto load_ids = [&](int chunk) {
+          const int t = (tile0 + chunk * per) * kTile + lane * p.box;
           int id = 0;
-          if (lane < boxes && t < end) {
+          if (chunk * per < n && t < end) {
             id = __ldg(table + a.by_page.of(t));
             if (id < 0 || id >= a.num_blocks) err |= SV_DEVERR_PAGE, id = 0;
           }
           return id;
         };
+        int chunk = 0, ids_before = 0, ids = load_ids(0), ids_after = load_ids(1);
         const int count = NS == 1 ? 2 * n : n;
         int ki = 0, vi = 0;
-        // the warp's next unit: whether it is a V, its tile's first key, its place
-        auto order = [&](bool* val, int* at) {
-          *val = NS == 2 ? side == 1 : ki == n || (ki >= 2 && ki == vi + 2);
-          const int i = *val ? vi++ : ki++;
-          *at = before + (*val ? v_position(n, i) : k_position(i));
-          return (tile0 + i) * kTile;
-        };
-        bool val, val_next = false;
-        int at, at_next = 0, t0 = order(&val, &at), t_next = 0, id = load_id(t0), id_next = 0;
         for (int x = 0; x < count; ++x) {
-          if (x + 1 < count) t_next = order(&val_next, &at_next), id_next = load_id(t_next);
+          // the warp's next unit: whether it is a V, its tile and its place
+          const bool val = NS == 2 ? side == 1 : ki == n || (ki >= 2 && ki == vi + 2);
+          const int i = val ? vi++ : ki++;
+          const int at = before + (val ? v_position(n, i) : k_position(i)), t0 = (tile0 + i) * kTile;
+          if (i >> shift > chunk) {
+            ++chunk;
+            ids_before = ids, ids = ids_after, ids_after = load_ids(chunk + 1);
+          }
+          const int id = __shfl_sync(~0u, i >> shift == chunk ? ids : ids_before,
+                                     (i & (per - 1)) * boxes + (lane / L::kChunks & (boxes - 1)));
           const int u = at % L::kUnits;
           if (at >= L::kUnits) mbar_wait(empty(u), (at / L::kUnits + 1) & 1, timed_out);
           __syncwarp();
-          const int live = max(0, min(boxes, (end - t0 + p.box - 1) / p.box));
+          const int live = max(0, min(boxes, (end - t0 + p.box - 1) >> (__ffs(p.box) - 1)));
           if (elect_one()) mbar_arrive_expect_tx(full(u), live * bytes);
           const uint32_t dst = ring_addr + u * L::kUnitBytes;
           if (boxes == 1) {
-            const int page = __shfl_sync(~0u, id, 0);
+            const int page = __shfl_sync(~0u, id, 0);  // for a uniform register
             const int in_page = t0 - a.by_page.of(t0) * a.page;
             if (live > 0 && elect_one()) {
 #pragma unroll
@@ -421,13 +429,11 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
             }
           } else {  // several small pages: a lane a copy
             const int b = lane / L::kChunks, c = lane % L::kChunks;
-            const int page = __shfl_sync(~0u, id, b);
             __syncwarp();
             if (b < live)
               tma_load4(dst + c * (kTile * 128) + b * p.box * 128, val ? &vmap : &kmap, c * 64, 0, head,
-                        page, full(u));
+                        id, full(u));
           }
-          t0 = t_next, val = val_next, at = at_next, id = id_next;
         }
         before += 2 * n;
       }

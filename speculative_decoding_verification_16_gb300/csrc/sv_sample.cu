@@ -799,6 +799,7 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
 
   // ---- one pass: every group's largest logit (NaN wins) and mass
   bool joined = false;
+  const uint32_t stat0 = peer_addr(R.stat, 0);
   auto group = [&](int i, const uint4& raw) {
     float m;
     if constexpr (ES == 2) {
@@ -808,8 +809,9 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
       const Vec<4> x(raw);
       m = fmax_nan(fmax_nan(x.x[0], x.x[1]), fmax_nan(x.x[2], x.x[3]));
     }
-    if (G == 32) {
-      m = float_of<4>(__reduce_max_sync(~0u, key_of<4>(m)));
+    if (G == 8) {  // the usual size, without a loop
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) m = fmax_nan(m, __shfl_xor_sync(~0u, m, d));
     } else {
       for (int d = 1; d < G; d <<= 1) m = fmax_nan(m, __shfl_xor_sync(~0u, m, d));
     }
@@ -819,15 +821,19 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
       const float ref = m == -kInf ? 0.0f : m;
 #pragma unroll
       for (int e = 0; e < N; ++e) s += weight_of(x.x[e], ref, R.sc);
-      for (int d = 1; d < G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
+      if (G == 8) {
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
+      } else {
+        for (int d = 1; d < G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
+      }
     }
     if (!joined) {  // every CTA of the row runs: rank 0's memory can be written
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       joined = true;
     }
     if ((lane & (G - 1)) == 0 && i < R.v1)
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
-                       peer_addr(R.stat + (i >> a.shift), 0)),
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(stat0 + (i >> a.shift) * 8),
                    "f"(m), "f"(s)
                    : "memory");
   };
@@ -960,17 +966,17 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
           // -- the cuts and the draw on the ranked list
           R.rank_list(listed);
           if (warp == 0) {
-            float kept, total;
+            float kept = row_mass, total = 0.0f;
             int keep = use_k ? top_k : listed;
-            R.reach(keep, kInf, &kept);
-            if (!use_k) kept = row_mass;
+            if (use_k) R.reach(keep, kInf, &kept);
+            total = kept;
             if (use_p) keep = R.reach(keep, top_p * kept, &total);
             if (min_p > 0.0f) {
               int c = 0;
               for (int i = lane; i < keep; i += 32) c += h->w[i] >= min_p ? 1 : 0;
               keep = __reduce_add_sync(~0u, c);
+              R.reach(keep, kInf, &total);
             }
-            R.reach(keep, kInf, &total);
             if (lane == 0) h->cut = keep, h->total = total, h->pick = INT32_MAX;
           }
           __syncthreads();
