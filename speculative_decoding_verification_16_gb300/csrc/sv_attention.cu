@@ -50,10 +50,13 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int r) {
   return s;
 }
 
-// ---------------------------------------------------------------- fp32
+// ---------------------------------------------------------------- rows
 //
-// One warp a (row, head): 32 keys at a time, a lane its own key's score, then
-// the lanes own the head's dimensions for the weighted sum of the values.
+// fp32, and bf16 heads above 128: one warp a (row, head).  32 keys at a time, a
+// lane its own key's score in 16-byte loads against the query in shared memory,
+// then the lanes own the head's dimensions for the weighted sum of the values.
+// All in 32 bits on the FMA pipes; keys and values are read once a row and head
+// (from L2 for the rows that share them).
 constexpr int kRowWarps = 4;
 
 template <typename T>
@@ -108,10 +111,18 @@ __global__ __launch_bounds__(kRowWarps * 32) void attn_rows_kernel(const AttnArg
         id = 0;
       }
       at = id * a.block + (t % a.page) * a.token + hoff;
-      const T* k = reinterpret_cast<const T*>(a.k + at);
-      float dot = 0;
-      for (int d = 0; d < a.dim; ++d) dot = fmaf(qs[warp][d], to_float(k[d]), dot);
-      x = dot * a.scale2;
+      constexpr int kPer = 16 / sizeof(T);
+      const uint4* k = reinterpret_cast<const uint4*>(a.k + at);
+      float dot[2] = {0, 0};
+#pragma unroll 4
+      for (int i = 0; i < a.dim / kPer; ++i) {
+        const uint4 raw = __ldg(k + i);
+        const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+        for (int d = 0; d < kPer; ++d)
+          dot[d & 1] = fmaf(qs[warp][i * kPer + d], to_float(e[d]), dot[d & 1]);
+      }
+      x = (dot[0] + dot[1]) * a.scale2;
     }
     float top = x;
 #pragma unroll
@@ -127,6 +138,7 @@ __global__ __launch_bounds__(kRowWarps * 32) void attn_rows_kernel(const AttnArg
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] *= keep;
     const int n = min(32, pos - t0 + 1);
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
       const float pj = __shfl_sync(~0u, p, j);
       const T* v = reinterpret_cast<const T*>(a.v + __shfl_sync(~0u, at, j));

@@ -22,6 +22,15 @@
 // A pass of the search ends with an exchange: each CTA stores its partial into
 // every CTA's shared memory, and after the cluster barrier all sum the C
 // partials in rank order, so all decide alike.
+//
+// What bounds it.  One row: latency (151,936 bf16 under top-k 20 and top-p 0.95
+// 8.6 us: 1.3 us to the settings, 1.8 us for the row on eight SMs, 0.9 us of
+// cluster barriers, 3.5 us to decide).  Many rows: the stream at two CTAs an SM with
+// the decision's latency between (512 rows of 262,144 bf16, 268 MB: 86 us, 3.1 TB/s,
+// 0.47 of the measured copy rate).  Rows that need the search: instructions, about
+// three passes over the row (96 flat fp32 rows of 129,280 under top-p 96 us).
+// Rows held in the cluster's shared memory instead of read again measured slower:
+// 180 us for the 512 rows, the resident bytes waiting through every decision.
 #include <cuda_runtime.h>
 
 #include <algorithm>
