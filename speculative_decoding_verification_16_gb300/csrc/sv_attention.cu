@@ -169,12 +169,12 @@ constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr size_t kRecordBytes = round256(sizeof(AttnRecord) * kMaxWorkers);
 constexpr size_t kMlBytes = sizeof(float2) * 2 * kMaxWorkers * kRows;
 
-bool on_tensor_cores(int dtype, int head_dim) { return dtype == SV_BF16 && head_dim <= 128; }
+int padded(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
 size_t workspace_bytes_of(int dtype, int head_dim) {
-  if (!on_tensor_cores(dtype, head_dim)) return 256;
-  const size_t dp = head_dim <= 64 ? 64 : 128;
-  return kRecordBytes + kMlBytes + sizeof(float) * 2 * kMaxWorkers * kRows * dp;
+  if (dtype != SV_BF16) return 256;
+  const size_t dp = padded(head_dim);
+  return kRecordBytes + kMlBytes + sizeof(float) * 2 * kMaxWorkers * kRows * (dp < 128 ? dp : 128);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -229,10 +229,11 @@ int launch_mma(const MmaArgs& p, int grid, int64_t items, int64_t joins, const C
   // items in two parts: more and smaller blocks, 163 us against 175
   if (grid >= 8 * items)
     return launch(attn_combine_kernel<NS * kRows, DP, 4>,
-                  dim3(static_cast<unsigned>(std::min<int64_t>(joins, 4 * d.sms))), 512, 0, 1, true, st,
+                  dim3(static_cast<unsigned>(std::min<int64_t>(joins, 4 * d.sms))), 4 * combine_group(DP), 0, 1, true, st,
                   p, grid);
   return launch(attn_combine_kernel<NS * kRows, DP, 1>,
-                dim3(static_cast<unsigned>(std::min<int64_t>(joins, 16 * d.sms))), 128, 0, 1, true, st, p,
+                dim3(static_cast<unsigned>(std::min<int64_t>(joins, 16 * d.sms))), combine_group(DP), 0, 1,
+                true, st, p,
                 grid);
 }
 
@@ -240,7 +241,7 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
   Device d;
   const int rc = device(&d);
   if (rc != SV_OK) return rc;
-  const int dp = a.dim <= 64 ? 64 : 128;
+  const int dp = padded(a.dim);
   char* ws = static_cast<char*>(workspace);
   MmaArgs p{a, kv_heads, 0, false, reinterpret_cast<AttnRecord*>(ws),
             reinterpret_cast<float2*>(ws + kRecordBytes),
@@ -258,19 +259,21 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
                     !encode_cache(&vm, a.v, a, kv_heads, p.box)))
     return SV_ERR_CUDA;
   const int64_t rows = std::min<int64_t>(a.max_len, a.n_rows) * a.group;
-  const int ns = rows > kRows ? 2 : 1;
+  const int ns = rows > kRows && dp <= 128 ? 2 : 1;
   const int64_t keys = static_cast<int64_t>(a.table_width) * a.page;
   // items of at most four tiles are not cut: the parts' latency and the second
   // launch would cost what they save
   p.whole = keys <= 4 * kTile;
   const int64_t tiles = (rows + ns * kRows - 1) / (ns * kRows) * (p.whole ? 1 : (keys + kTile - 1) / kTile) *
                         a.B * kv_heads;
-  const int64_t most = ns == 1 ? std::min(2 * d.sms, kMaxWorkers) : std::min(d.sms, kMaxWorkers / 2);
+  const int per_sm = attn_per_sm(ns, dp);
+  const int64_t most = std::min(per_sm * d.sms, per_sm * kMaxWorkers / 2);
   const int grid = static_cast<int>(std::min(most, tiles));
   // row groups of the items that can be cut: a block each
   const int64_t items = (rows + ns * kRows - 1) / (ns * kRows) * a.B * kv_heads;
   const int64_t joins = std::min<int64_t>(items, grid - 1) *
                         ((std::min<int64_t>(rows, ns * kRows) + kCombineRows - 1) / kCombineRows);
+  if (dp == 256) return launch_mma<1, 256>(p, grid, items, joins, km, vm, st);
   if (ns == 1)
     return dp == 64 ? launch_mma<1, 64>(p, grid, items, joins, km, vm, st) : launch_mma<1, 128>(p, grid, items, joins, km, vm, st);
   return dp == 64 ? launch_mma<2, 64>(p, grid, items, joins, km, vm, st) : launch_mma<2, 128>(p, grid, items, joins, km, vm, st);
@@ -338,11 +341,10 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
                    dev_error, FastDiv::by(static_cast<uint32_t>(heads / kv_heads)),
                    FastDiv::by(static_cast<uint32_t>(page_size))};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (on_tensor_cores(dtype, head_dim)) return run_mma(a, kv_heads, workspace, st);
+  if (dtype == SV_BF16) return run_mma(a, kv_heads, workspace, st);
   const int64_t items = static_cast<int64_t>(n_rows) * heads;
   const dim3 grid(static_cast<unsigned>((items + kRowWarps - 1) / kRowWarps));
-  return es == 2 ? launch(attn_rows_kernel<__nv_bfloat16>, grid, kRowWarps * 32, 0, 1, false, st, a)
-                 : launch(attn_rows_kernel<float>, grid, kRowWarps * 32, 0, 1, false, st, a);
+  return launch(attn_rows_kernel<float>, grid, kRowWarps * 32, 0, 1, false, st, a);
 }
 
 }  // extern "C"

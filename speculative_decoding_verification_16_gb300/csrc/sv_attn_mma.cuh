@@ -1,4 +1,4 @@
-// sv_attn_mma.cuh -- the tensor core attention kernel (bf16, head_dim <= 128).
+// sv_attn_mma.cuh -- the tensor core attention kernel (bf16).
 //
 // The query rows of a request that share a key/value head -- l tokens times the
 // group of G heads -- are packed into tiles of 128 rows, row i = token i / G,
@@ -24,7 +24,8 @@
 // full rate.
 //
 // NS = 1 (at most 128 rows an item, decoding and verify steps: the cache's
-// bytes bound it): two CTAs an SM, each with one stream.
+// bytes bound it): two CTAs an SM, each with one stream; for heads above 128, whose
+// O fills half the tensor memory, one CTA an SM at any number of rows.
 // NS = 2 (longer chunks: the products bound it): one CTA an SM, two streams
 // over the same key/value tiles, the tensor core alternating between them.
 //
@@ -50,7 +51,7 @@ namespace serve {
 
 constexpr int kRows = 128;        // query rows of a stream
 constexpr int kTile = 64;         // keys of a tile
-constexpr int kMaxWorkers = 320;  // partials are laid out for this many
+constexpr int kMaxWorkers = 320;  // most CTAs of heads up to 128 with one stream
 constexpr int kMinRun = 3;        // least tiles of a worker's run
 constexpr float kRescale = 8.0f;  // log2 of how far P may exceed 1 before O is rescaled
 
@@ -69,7 +70,9 @@ struct MmaArgs {
 };
 
 constexpr int kMaxUnits = 10;
-__host__ __device__ constexpr int attn_units(int ns, int dp) { return ns == 1 && dp == 128 ? 5 : kMaxUnits; }
+__host__ __device__ constexpr int attn_units(int ns, int dp) { return ns == 1 && dp >= 128 ? 5 : kMaxUnits; }
+// CTAs an SM.
+__host__ __device__ constexpr int attn_per_sm(int ns, int dp) { return ns == 1 && dp <= 128 ? 2 : 1; }
 __host__ __device__ constexpr int attn_threads(int ns) { return ns * 6 * 32; }  // softmax, copies, products
 // query tiles, ring of key and value tiles, barriers, the softmax warps' walks
 __host__ __device__ constexpr int attn_smem(int ns, int dp) {
@@ -314,13 +317,13 @@ struct WarpWalk {
 };
 
 template <int NS, int DP, bool TMA>
-__global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
+__global__ __launch_bounds__(attn_threads(NS), attn_per_sm(NS, DP)) void attn_mma_kernel(
     const MmaArgs p, const __grid_constant__ CUtensorMap kmap,
     const __grid_constant__ CUtensorMap vmap) {
   using L = AttnSmem<NS, DP>;
   constexpr int MR = NS * kRows;
   constexpr int kThreads = attn_threads(NS);
-  constexpr uint32_t kCols = NS == 1 ? 256 : 512;
+  constexpr uint32_t kCols = attn_per_sm(NS, DP) == 2 ? 256 : 512;
   // tensor memory columns: two S buffers of each stream, then O of each
   constexpr uint32_t kO = NS * 2 * kTile;
   extern __shared__ __align__(1024) char smem[];
@@ -872,12 +875,16 @@ __global__ __launch_bounds__(attn_threads(NS), 3 - NS) void attn_mma_kernel(
 // and by the partials' bytes (from L2) where there are many.
 constexpr int kCombineRows = 4;
 
+// threads of a group: four rows of DP / 4 columns, a whole number of warps per row
+__host__ __device__ constexpr int combine_group(int dp) { return dp < 128 ? 128 : dp; }
+
 template <int MR, int DP, int GROUPS>
-__global__ __launch_bounds__(GROUPS * 128) void attn_combine_kernel(const MmaArgs p, int workers) {
-  constexpr int kCombineThreads = GROUPS * 128, kCombineGroups = GROUPS;
+__global__ __launch_bounds__(GROUPS * combine_group(DP)) void attn_combine_kernel(const MmaArgs p,
+                                                                                  int workers) {
+  constexpr int kGroup = combine_group(DP), kCombineThreads = GROUPS * kGroup, kCombineGroups = GROUPS;
   __shared__ AttnRecord item[kMaxWorkers];
   __shared__ int32_t second[kMaxWorkers];  // the item's second worker
-  __shared__ float4 sums[GROUPS > 1 ? GROUPS - 1 : 1][128];
+  __shared__ float4 sums[GROUPS > 1 ? GROUPS - 1 : 1][kGroup];
   __shared__ float weight[kCombineRows][kMaxWorkers], inverse[kCombineRows];
   __shared__ int32_t found[(kMaxWorkers + kCombineThreads - 1) / kCombineThreads * (kCombineThreads / 32)];
   const AttnArgs& a = p.a;
@@ -919,7 +926,7 @@ __global__ __launch_bounds__(GROUPS * 128) void attn_combine_kernel(const MmaArg
     auto slot = [&](int i) { return static_cast<int64_t>(2 * (w0 + i) + (i == 0 ? 1 : 0)); };
     // thread: row row0 + tid % 4, columns [4 q, 4 q + 4), parts group, group + 4, ..;
     // the first parts' loads go out before the weights are known
-    const int sub = tid % kCombineRows, q = tid / kCombineRows % 32, group = tid / 128,
+    const int sub = tid % kCombineRows, q = tid / kCombineRows % (kGroup / 4), group = tid / kGroup,
               mine_row = row0 + sub;
     const bool on = mine_row < rows && q * 4 < a.dim;
     auto load = [&](int i) { return p.o[(slot(i) * (DP / 4) + q) * MR + mine_row]; };
@@ -969,7 +976,7 @@ __global__ __launch_bounds__(GROUPS * 128) void attn_combine_kernel(const MmaArg
         }
     }
     if (GROUPS > 1) {
-      if (group > 0) sums[group - 1][tid % 128] = o;
+      if (group > 0) sums[group - 1][tid % kGroup] = o;
       __syncthreads();
     }
     if (on && group == 0) {
