@@ -50,116 +50,10 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int r) {
   return s;
 }
 
-// ---------------------------------------------------------------- rows
-//
-// fp32, and bf16 heads above 128: one warp a (row, head).  32 keys at a time, a
-// lane its own key's score in 16-byte loads against the query in shared memory,
-// then the lanes own the head's dimensions for the weighted sum of the values.
-// All in 32 bits on the FMA pipes; keys and values are read once a row and head
-// (from L2 for the rows that share them).
-constexpr int kRowWarps = 4;
-
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ float from_float(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
-
-template <typename T>
-__global__ __launch_bounds__(kRowWarps * 32) void attn_rows_kernel(const AttnArgs a) {
-  __shared__ float qs[kRowWarps][SV_ATTN_MAX_HEAD_DIM];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
-  const int row = static_cast<int>(item / a.heads), h = static_cast<int>(item % a.heads);
-  if (row >= a.n_rows) return;
-  int lo = 0, hi = a.B;  // the request: last r with row_offsets[r] <= row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.row_offsets[mid] <= row) lo = mid; else hi = mid;
-  }
-  const Span s = span_of(a, lo);
-  if (s.l < 0) {
-    if (lane == 0 && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_LEN);
-    return;
-  }
-  if (row < s.row0 || row >= s.row0 + s.l) return;
-  const T* q = reinterpret_cast<const T*>(a.q + row * a.q_row + h * a.q_head);
-  for (int d = lane; d < a.dim; d += 32) qs[warp][d] = to_float(q[d]);
-  __syncwarp();
-  const int pos = s.seq - s.l + row - s.row0;
-  const int first = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  const int64_t hoff = (h / a.group) * a.head;
-  constexpr int kPer = SV_ATTN_MAX_HEAD_DIM / 32;
-  float m = -kInf, z = 0, o[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = 0;
-  for (int t0 = first; t0 <= pos; t0 += 32) {
-    const int t = t0 + lane;
-    int64_t at = 0;
-    float x = -kInf;
-    if (t <= pos) {
-      int id = a.table[lo * a.table_stride + t / a.page];
-      if (id < 0 || id >= a.num_blocks) {
-        if (a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_PAGE);
-        id = 0;
-      }
-      at = id * a.block + (t % a.page) * a.token + hoff;
-      constexpr int kPer = 16 / sizeof(T);
-      const uint4* k = reinterpret_cast<const uint4*>(a.k + at);
-      float dot[2] = {0, 0};
-#pragma unroll 4
-      for (int i = 0; i < a.dim / kPer; ++i) {
-        const uint4 raw = __ldg(k + i);
-        const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-        for (int d = 0; d < kPer; ++d)
-          dot[d & 1] = fmaf(qs[warp][i * kPer + d], to_float(e[d]), dot[d & 1]);
-      }
-      x = (dot[0] + dot[1]) * a.scale2;
-    }
-    float top = x;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    const float next = fmaxf(m, top);
-    const float base = next == -kInf ? 0.0f : next;
-    const float p = ex2(x - base), keep = ex2(m - base);
-    float sum = p;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-    z = z * keep + sum;
-    m = next;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] *= keep;
-    const int n = min(32, pos - t0 + 1);
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const float pj = __shfl_sync(~0u, p, j);
-      const T* v = reinterpret_cast<const T*>(a.v + __shfl_sync(~0u, at, j));
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i * 32 + lane < a.dim) o[i] = fmaf(pj, to_float(v[i * 32 + lane]), o[i]);
-    }
-  }
-  T* out = reinterpret_cast<T*>(a.out + row * a.o_row + h * a.o_head);
-  const bool none = pos < 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (i * 32 + lane < a.dim) out[i * 32 + lane] = from_float<T>(none ? 0.0f : o[i] / z);
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[static_cast<int64_t>(row) * a.heads + h] = none ? -kInf : (m + log2f(z)) * kLn2;
-}
-
 }  // namespace serve
 }  // namespace sv
 
-#include "sv_attn_mma.cuh"
+#include "sv_attn_fma.cuh"
 
 namespace sv {
 namespace serve {
@@ -172,8 +66,10 @@ constexpr size_t kMlBytes = sizeof(float2) * 2 * kMaxWorkers * kRows;
 int padded(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
 size_t workspace_bytes_of(int dtype, int head_dim) {
-  if (dtype != SV_BF16) return 256;
   const size_t dp = padded(head_dim);
+  if (dtype == SV_FP32)
+    return kRecordBytes + sizeof(float2) * 2 * kMaxWorkers * kFmaRows +
+           sizeof(float) * 2 * kMaxWorkers * kFmaRows * dp;
   return kRecordBytes + kMlBytes + sizeof(float) * 2 * kMaxWorkers * kRows * (dp < 128 ? dp : 128);
 }
 
@@ -213,6 +109,25 @@ bool encode_cache(CUtensorMap* map, const void* base, const AttnArgs& a, int kv_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Joins the items that `grid` workers were given in parts.
+template <int MR, int DP, bool F32>
+int join(const MmaArgs& p, int grid, int64_t items, int64_t joins, cudaStream_t st) {
+  if (grid == 1 || p.whole) return SV_OK;  // no item is cut
+  Device d;
+  const int rc = device(&d);
+  if (rc != SV_OK) return rc;
+  // few items in many parts (one request's verify step: 8 items in 21): four
+  // threads a column take a part of them each, 17.6 us a call against 23.8; many
+  // items in two parts: more and smaller blocks, 163 us against 175
+  if (grid >= 8 * items)
+    return launch(attn_combine_kernel<MR, DP, 4, F32>,
+                  dim3(static_cast<unsigned>(std::min<int64_t>(joins, 4 * d.sms))),
+                  4 * combine_group(DP), 0, 1, true, st, p, grid);
+  return launch(attn_combine_kernel<MR, DP, 1, F32>,
+                dim3(static_cast<unsigned>(std::min<int64_t>(joins, 16 * d.sms))), combine_group(DP),
+                0, 1, true, st, p, grid);
+}
+
 template <int NS, int DP>
 int launch_mma(const MmaArgs& p, int grid, int64_t items, int64_t joins, const CUtensorMap& km,
                const CUtensorMap& vm, cudaStream_t st) {
@@ -220,21 +135,29 @@ int launch_mma(const MmaArgs& p, int grid, int64_t items, int64_t joins, const C
   int rc = p.box > 0
                ? launch(attn_mma_kernel<NS, DP, true>, dim3(grid), threads, smem, 1, false, st, p, km, vm)
                : launch(attn_mma_kernel<NS, DP, false>, dim3(grid), threads, smem, 1, false, st, p, km, vm);
-  if (rc != SV_OK || grid == 1 || p.whole) return rc;  // no item is cut
-  Device d;
-  rc = device(&d);
-  if (rc != SV_OK) return rc;
-  // few items in many parts (one request's verify step: 8 items in 38): four
-  // threads a column take a part of them each, 17.6 us a call against 23.8; many
-  // items in two parts: more and smaller blocks, 163 us against 175
-  if (grid >= 8 * items)
-    return launch(attn_combine_kernel<NS * kRows, DP, 4>,
-                  dim3(static_cast<unsigned>(std::min<int64_t>(joins, 4 * d.sms))), 4 * combine_group(DP), 0, 1, true, st,
-                  p, grid);
-  return launch(attn_combine_kernel<NS * kRows, DP, 1>,
-                dim3(static_cast<unsigned>(std::min<int64_t>(joins, 16 * d.sms))), combine_group(DP), 0, 1,
-                true, st, p,
-                grid);
+  return rc != SV_OK ? rc : join<NS * kRows, DP, false>(p, grid, items, joins, st);
+}
+
+// What a call's sizes bound: the row tiles' items and their key tiles.
+struct Bounds {
+  int64_t items, joins;
+  int grid;
+};
+Bounds bounds(MmaArgs* p, int tile_rows, int64_t most) {
+  const AttnArgs& a = p->a;
+  const int64_t rows = std::min<int64_t>(a.max_len, a.n_rows) * a.group;
+  const int64_t keys = static_cast<int64_t>(a.table_width) * a.page;
+  // items of at most four tiles are not cut: the parts' latency and the second
+  // launch would cost what they save
+  p->whole = keys <= 4 * kTile;
+  Bounds b;
+  b.items = (rows + tile_rows - 1) / tile_rows * a.B * p->kv_heads;
+  b.grid = static_cast<int>(
+      std::min(most, b.items * (p->whole ? 1 : (keys + kTile - 1) / kTile)));
+  // row groups of the items that can be cut: a block each
+  b.joins = std::min<int64_t>(b.items, b.grid - 1) *
+            ((std::min<int64_t>(rows, tile_rows) + kCombineRows - 1) / kCombineRows);
+  return b;
 }
 
 int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
@@ -259,24 +182,38 @@ int run_mma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
                     !encode_cache(&vm, a.v, a, kv_heads, p.box)))
     return SV_ERR_CUDA;
   const int64_t rows = std::min<int64_t>(a.max_len, a.n_rows) * a.group;
-  const int ns = rows > kRows && dp <= 128 ? 2 : 1;
-  const int64_t keys = static_cast<int64_t>(a.table_width) * a.page;
-  // items of at most four tiles are not cut: the parts' latency and the second
-  // launch would cost what they save
-  p.whole = keys <= 4 * kTile;
-  const int64_t tiles = (rows + ns * kRows - 1) / (ns * kRows) * (p.whole ? 1 : (keys + kTile - 1) / kTile) *
-                        a.B * kv_heads;
-  const int per_sm = attn_per_sm(ns, dp);
-  const int64_t most = std::min(per_sm * d.sms, per_sm * kMaxWorkers / 2);
-  const int grid = static_cast<int>(std::min(most, tiles));
-  // row groups of the items that can be cut: a block each
-  const int64_t items = (rows + ns * kRows - 1) / (ns * kRows) * a.B * kv_heads;
-  const int64_t joins = std::min<int64_t>(items, grid - 1) *
-                        ((std::min<int64_t>(rows, ns * kRows) + kCombineRows - 1) / kCombineRows);
-  if (dp == 256) return launch_mma<1, 256>(p, grid, items, joins, km, vm, st);
+  const int ns = rows > kRows && dp <= 128 ? 2 : 1, per_sm = attn_per_sm(ns, dp);
+  const Bounds b = bounds(&p, ns * kRows, std::min(per_sm * d.sms, per_sm * kMaxWorkers / 2));
+  if (dp == 256) return launch_mma<1, 256>(p, b.grid, b.items, b.joins, km, vm, st);
   if (ns == 1)
-    return dp == 64 ? launch_mma<1, 64>(p, grid, items, joins, km, vm, st) : launch_mma<1, 128>(p, grid, items, joins, km, vm, st);
-  return dp == 64 ? launch_mma<2, 64>(p, grid, items, joins, km, vm, st) : launch_mma<2, 128>(p, grid, items, joins, km, vm, st);
+    return dp == 64 ? launch_mma<1, 64>(p, b.grid, b.items, b.joins, km, vm, st)
+                    : launch_mma<1, 128>(p, b.grid, b.items, b.joins, km, vm, st);
+  return dp == 64 ? launch_mma<2, 64>(p, b.grid, b.items, b.joins, km, vm, st)
+                  : launch_mma<2, 128>(p, b.grid, b.items, b.joins, km, vm, st);
+}
+
+template <int DP>
+int launch_fma(const MmaArgs& p, const Bounds& b, cudaStream_t st) {
+  const int rc =
+      launch(attn_fma_kernel<DP>, dim3(b.grid), kFmaThreads, fma_smem(DP), 1, false, st, p);
+  return rc != SV_OK ? rc : join<kFmaRows, DP, true>(p, b.grid, b.items, b.joins, st);
+}
+
+int run_fma(const AttnArgs& a, int kv_heads, void* workspace, cudaStream_t st) {
+  Device d;
+  const int rc = device(&d);
+  if (rc != SV_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  MmaArgs p{a, kv_heads, 0, false, reinterpret_cast<AttnRecord*>(ws),
+            reinterpret_cast<float2*>(ws + kRecordBytes),
+            reinterpret_cast<float4*>(ws + kRecordBytes +
+                                      sizeof(float2) * 2 * kMaxWorkers * kFmaRows)};
+  // shared memory holds one CTA an SM for heads above 128, else two
+  const int dp = padded(a.dim), per_sm = dp == 256 ? 1 : 2;
+  const Bounds b = bounds(&p, kFmaRows, std::min(per_sm * d.sms, kMaxWorkers));
+  return dp == 64    ? launch_fma<64>(p, b, st)
+         : dp == 128 ? launch_fma<128>(p, b, st)
+                     : launch_fma<256>(p, b, st);
 }
 
 }  // namespace
@@ -342,9 +279,7 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
                    FastDiv::by(static_cast<uint32_t>(page_size))};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == SV_BF16) return run_mma(a, kv_heads, workspace, st);
-  const int64_t items = static_cast<int64_t>(n_rows) * heads;
-  const dim3 grid(static_cast<unsigned>((items + kRowWarps - 1) / kRowWarps));
-  return launch(attn_rows_kernel<float>, grid, kRowWarps * 32, 0, 1, false, st, a);
+  return run_fma(a, kv_heads, workspace, st);
 }
 
 }  // extern "C"

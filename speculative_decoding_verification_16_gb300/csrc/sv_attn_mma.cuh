@@ -878,7 +878,7 @@ constexpr int kCombineRows = 4;
 // threads of a group: four rows of DP / 4 columns, a whole number of warps per row
 __host__ __device__ constexpr int combine_group(int dp) { return dp < 128 ? 128 : dp; }
 
-template <int MR, int DP, int GROUPS>
+template <int MR, int DP, int GROUPS, bool F32>
 __global__ __launch_bounds__(GROUPS * combine_group(DP)) void attn_combine_kernel(const MmaArgs p,
                                                                                   int workers) {
   constexpr int kGroup = combine_group(DP), kCombineThreads = GROUPS * kGroup, kCombineGroups = GROUPS;
@@ -987,12 +987,18 @@ __global__ __launch_bounds__(GROUPS * combine_group(DP)) void attn_combine_kerne
       }
       const float inv = inverse[sub];
       const int j = r.m * MR + mine_row;
-      uint2 v;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(o.y * inv), "f"(o.x * inv));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(o.w * inv), "f"(o.z * inv));
       const int64_t orow = static_cast<int64_t>(r.row0) + a.by_group.of(j);
       const int head = r.h * a.group + j - a.by_group.of(j) * a.group;
-      *reinterpret_cast<uint2*>(a.out + orow * a.o_row + head * a.o_head + q * 8) = v;
+      char* out = a.out + orow * a.o_row + head * a.o_head;
+      if constexpr (F32) {
+        *reinterpret_cast<float4*>(out + q * 16) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      } else {
+        uint2 v;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(o.y * inv), "f"(o.x * inv));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(o.w * inv), "f"(o.z * inv));
+        *reinterpret_cast<uint2*>(out + q * 8) = v;
+      }
     }
   }
 }

@@ -387,6 +387,16 @@ def test_attention_long(cuda_lib, G, l):
     check_attention(cuda_lib, BF, [(9001, l), (20000, l), (37, l), (4096, l)], 2, G, 128, 32, seed=l)
 
 
+@pytest.mark.parametrize("D", [64, 96, 256])
+@pytest.mark.parametrize("page", [1, 24, 64])
+@pytest.mark.parametrize("layout", ["tokens", "heads"])
+def test_attention_float_long(cuda_lib, D, page, layout):
+    """fp32: requests cut into many parts, ragged pages, strided rows, both layouts."""
+    lens = [(3001, 1), (37, 5), (5000, 16), (4096, 3)]
+    check_attention(cuda_lib, F32, lens, 2, 3, D, page, layout=layout, strided=True, seed=page)
+    check_attention(cuda_lib, F32, lens, 1, 2, D, page, layout=layout, window=300, seed=page)
+
+
 def test_attention_many_requests(cuda_lib):
     rng = np.random.default_rng(9)
     lens = [(int(n), int(min(n, l))) for n, l in zip(rng.integers(1, 400, 700),
