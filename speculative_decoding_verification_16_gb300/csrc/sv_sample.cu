@@ -190,22 +190,29 @@ struct Row {
   // vectors of the row are loaded without a branch; its first and last one and
   // what lies past the slice (-inf) are put right after.
   static constexpr int kLoads = 4;
+  __device__ __forceinline__ bool whole(int i0) const {  // nothing to put right
+    return i0 >= (lead > 0 ? 1 : 0) &&
+           i0 + (kLoads - 1) * kThreads + 32 <= min((lead + V) / N, v1);
+  }
   __device__ __forceinline__ void fetch(int i0, uint4* x) const {
     const int in0 = lead > 0 ? 1 : 0, in1 = (lead + V) / N, i = i0 + (threadIdx.x & 31);
     const uint4* p = reinterpret_cast<const uint4*>(base);
     const uint32_t pad = ES == 2 ? 0xff80ff80u : 0xff800000u;
+    if (whole(i0)) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) x[k] = __ldg(p + i + k * kThreads);
+      return;
+    }
     if (in1 > in0) {
 #pragma unroll
       for (int k = 0; k < kLoads; ++k)
         x[k] = __ldg(p + max(min(i + k * kThreads, min(in1, v1) - 1), in0));
     }
-    if (i0 < in0 || i0 + (kLoads - 1) * kThreads + 32 > min(in1, v1)) {
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int j = i + k * kThreads;
-        if (j >= v1) x[k] = make_uint4(pad, pad, pad, pad);
-        else if (j < in0 || j >= in1) x[k] = load(j);
-      }
+    for (int k = 0; k < kLoads; ++k) {
+      const int j = i + k * kThreads;
+      if (j >= v1) x[k] = make_uint4(pad, pad, pad, pad);
+      else if (j < in0 || j >= in1) x[k] = load(j);
     }
   }
   __device__ __forceinline__ int start() const { return v0 + (threadIdx.x >> 5) * 32; }
@@ -846,11 +853,72 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
                    "f"(m), "f"(s)
                    : "memory");
   };
+  // Four vectors of a lane at once, groups of 8: at each of three exchanges a lane
+  // hands over half of what it has, so lane 4 j + q of the group ends with vector
+  // pick(q)'s result in four exchanges, where one by one it takes twelve.
+  const int pick = (lane & 1) * 2 + (lane >> 1 & 1);
+  auto fold = [&](float v0, float v1, float v2, float v3, auto op) {
+    const bool odd = lane & 1, second = lane & 2;
+    const float p = __shfl_xor_sync(~0u, odd ? v0 : v2, 1), q = __shfl_xor_sync(~0u, odd ? v1 : v3, 1);
+    const float a = op(odd ? v2 : v0, p), b = op(odd ? v3 : v1, q);
+    const float c = op(second ? b : a, __shfl_xor_sync(~0u, second ? a : b, 2));
+    return op(c, __shfl_xor_sync(~0u, c, 4));
+  };
+  auto four = [&](int i0, const uint4* raw) {
+    float v[4];
+    float m;
+    if constexpr (ES == 2) {
+      uint32_t b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        b[k] = bf16x2_max_nan(bf16x2_max_nan(raw[k].x, raw[k].y), bf16x2_max_nan(raw[k].z, raw[k].w));
+      const float f = fold(__uint_as_float(b[0]), __uint_as_float(b[1]), __uint_as_float(b[2]),
+                           __uint_as_float(b[3]), [](float x, float y) {
+                             return __uint_as_float(
+                                 bf16x2_max_nan(__float_as_uint(x), __float_as_uint(y)));
+                           });
+      m = fmax_nan(bf16lo(__float_as_uint(f)), bf16hi(__float_as_uint(f)));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const Vec<4> x(raw[k]);
+        v[k] = fmax_nan(fmax_nan(x.x[0], x.x[1]), fmax_nan(x.x[2], x.x[3]));
+      }
+      m = fold(v[0], v[1], v[2], v[3], [](float x, float y) { return fmax_nan(x, y); });
+    }
+    float s = 0;
+    if (need_mass) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // lane with pick = k
+        const float top = __shfl_sync(~0u, m, (lane & 24) | (k >> 1) | (k & 1) << 1);
+        const float ref = top == -kInf ? 0.0f : top;
+        const Vec<ES> x(raw[k]);
+        v[k] = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[k] += weight_of(x.x[e], ref, R.sc);
+      }
+      s = fold(v[0], v[1], v[2], v[3], [](float x, float y) { return x + y; });
+    }
+    if (!joined) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      joined = true;
+    }
+    if ((lane & 4) == 0)
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                       stat0 + (i0 + pick * kThreads + lane) / 8 * 8),
+                   "f"(m), "f"(s)
+                   : "memory");
+  };
   for (int i0 = i_first; i0 < R.v1; i0 += kThreads * Row<ES>::kLoads) {
     uint4 x[Row<ES>::kLoads];
 #pragma unroll
     for (int k = 0; k < Row<ES>::kLoads; ++k) x[k] = ahead[k];
     if (i0 + kThreads * Row<ES>::kLoads < R.v1) R.fetch(i0 + kThreads * Row<ES>::kLoads, ahead);
+    if (G == 8 && R.whole(i0)) {
+      four(i0, x);
+      continue;
+    }
 #pragma unroll
     for (int k = 0; k < Row<ES>::kLoads; ++k)
       if (i0 + k * kThreads < R.v1) group(i0 + k * kThreads + lane, x[k]);
