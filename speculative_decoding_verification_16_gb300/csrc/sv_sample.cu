@@ -139,6 +139,19 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
   return v;
 }
+// Four vectors' values of a lane reduced over groups of 8 lanes: at each exchange a
+// lane hands over half of what it has, so it ends with the result of vector
+// folded(lane), after four exchanges for all; one by one they take twelve.
+__device__ __forceinline__ int folded(int lane) { return (lane & 1) * 2 + (lane >> 1 & 1); }
+template <typename Op>
+__device__ __forceinline__ float fold(const float* v, Op op) {
+  const bool odd = threadIdx.x & 1, second = threadIdx.x & 2;
+  const float p = __shfl_xor_sync(~0u, odd ? v[0] : v[2], 1);
+  const float q = __shfl_xor_sync(~0u, odd ? v[1] : v[3], 1);
+  const float a = op(odd ? v[2] : v[0], p), b = op(odd ? v[3] : v[1], q);
+  const float c = op(second ? b : a, __shfl_xor_sync(~0u, second ? a : b, 2));
+  return op(c, __shfl_xor_sync(~0u, c, 4));
+}
 // A token in a list: larger is better (value desc, id asc; zeros alike).
 __device__ __forceinline__ uint64_t entry_of(float x, int id) {
   const uint32_t b = __float_as_uint(x + 0.0f);
@@ -388,12 +401,17 @@ __device__ __noinline__ Cut cut_by_bins(Row<ES> R, int k, float need, Cut within
   const bool by_mass = need >= 0.0f;
   Header* h = R.h;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float origin = top_x < kInf ? top_x : R.best, step = R.sc * 64.0f;
-  auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>((origin - x) * step)); };
-  const float low = fmaxf(floor_x, within.t);
-  const bool ties = within.id != INT32_MAX;  // of tokens at within.t only some count
+  const float origin = top_x < kInf ? top_x : R.best, step = fminf(R.sc * 64.0f, 3.0e38f);
+  // rounded to the nearest by an addition (conversions run at a quarter of its rate)
+  auto bin_of = [&](float x) {
+    return __float_as_int(fminf(fmaf(origin - x, step, 0x1p23f), 0x1p23f + (kBins - 1))) -
+           __float_as_int(0x1p23f);
+  };
+  const float low = fmaxf(fmaxf(floor_x, within.t), -3.4028235e38f);
+  // of tokens at within.t only some may count; NaN: all do
+  const float tie = within.id != INT32_MAX ? within.t : __int_as_float(0x7fc00000);
   auto inside = [&](float x, int id) {
-    return (x < top_x) & (x >= low) & (x > -kInf) & (!ties | (x > within.t) | (id <= within.id));
+    return (x < top_x) & (x >= low) && !(x == tie && id > within.id);
   };
   for (int i = tid; i < kBins; i += kThreads) h->bins[i] = 0;
   __syncthreads();
@@ -423,7 +441,7 @@ __device__ __noinline__ Cut cut_by_bins(Row<ES> R, int k, float need, Cut within
     int c = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      mass[j] = static_cast<float>(n[j]) * w0 * ex2(-(tid * kPer + j + 0.5f) / 64.0f);
+      mass[j] = static_cast<float>(n[j]) * w0 * ex2(-(tid * kPer + j) / 64.0f);
       m += mass[j], c += n[j];
     }
     float mi = m;
@@ -816,6 +834,12 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
   // ---- one pass: every group's largest logit (NaN wins) and mass
   bool joined = false;
   const uint32_t stat0 = peer_addr(R.stat, 0);
+  auto join = [&] {  // every CTA of the row runs: rank 0's memory can be written
+    if (!joined) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      joined = true;
+    }
+  };
   auto group = [&](int i, const uint4& raw) {
     float m;
     if constexpr (ES == 2) {
@@ -825,72 +849,45 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
       const Vec<4> x(raw);
       m = fmax_nan(fmax_nan(x.x[0], x.x[1]), fmax_nan(x.x[2], x.x[3]));
     }
-    if (G == 8) {  // the usual size, without a loop
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) m = fmax_nan(m, __shfl_xor_sync(~0u, m, d));
-    } else {
-      for (int d = 1; d < G; d <<= 1) m = fmax_nan(m, __shfl_xor_sync(~0u, m, d));
-    }
+    for (int d = 1; d < G; d <<= 1) m = fmax_nan(m, __shfl_xor_sync(~0u, m, d));
     float s = 0;
     if (need_mass) {
       const Vec<ES> x(raw);
       const float ref = m == -kInf ? 0.0f : m;
 #pragma unroll
       for (int e = 0; e < N; ++e) s += weight_of(x.x[e], ref, R.sc);
-      if (G == 8) {
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
-      } else {
-        for (int d = 1; d < G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
-      }
+      for (int d = 1; d < G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
     }
-    if (!joined) {  // every CTA of the row runs: rank 0's memory can be written
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-      joined = true;
-    }
+    join();
     if ((lane & (G - 1)) == 0 && i < R.v1)
       asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(stat0 + (i >> a.shift) * 8),
                    "f"(m), "f"(s)
                    : "memory");
   };
-  // Four vectors of a lane at once, groups of 8: at each of three exchanges a lane
-  // hands over half of what it has, so lane 4 j + q of the group ends with vector
-  // pick(q)'s result in four exchanges, where one by one it takes twelve.
-  const int pick = (lane & 1) * 2 + (lane >> 1 & 1);
-  auto fold = [&](float v0, float v1, float v2, float v3, auto op) {
-    const bool odd = lane & 1, second = lane & 2;
-    const float p = __shfl_xor_sync(~0u, odd ? v0 : v2, 1), q = __shfl_xor_sync(~0u, odd ? v1 : v3, 1);
-    const float a = op(odd ? v2 : v0, p), b = op(odd ? v3 : v1, q);
-    const float c = op(second ? b : a, __shfl_xor_sync(~0u, second ? a : b, 2));
-    return op(c, __shfl_xor_sync(~0u, c, 4));
-  };
+  // the usual size, 8 vectors a group, four groups at once
   auto four = [&](int i0, const uint4* raw) {
-    float v[4];
-    float m;
+    float v[4], m;
     if constexpr (ES == 2) {
-      uint32_t b[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        b[k] = bf16x2_max_nan(bf16x2_max_nan(raw[k].x, raw[k].y), bf16x2_max_nan(raw[k].z, raw[k].w));
-      const float f = fold(__uint_as_float(b[0]), __uint_as_float(b[1]), __uint_as_float(b[2]),
-                           __uint_as_float(b[3]), [](float x, float y) {
-                             return __uint_as_float(
-                                 bf16x2_max_nan(__float_as_uint(x), __float_as_uint(y)));
-                           });
-      m = fmax_nan(bf16lo(__float_as_uint(f)), bf16hi(__float_as_uint(f)));
+        v[k] = __uint_as_float(bf16x2_max_nan(bf16x2_max_nan(raw[k].x, raw[k].y),
+                                              bf16x2_max_nan(raw[k].z, raw[k].w)));
+      const uint32_t f = __float_as_uint(fold(v, [](float x, float y) {
+        return __uint_as_float(bf16x2_max_nan(__float_as_uint(x), __float_as_uint(y)));
+      }));
+      m = fmax_nan(bf16lo(f), bf16hi(f));
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const Vec<4> x(raw[k]);
         v[k] = fmax_nan(fmax_nan(x.x[0], x.x[1]), fmax_nan(x.x[2], x.x[3]));
       }
-      m = fold(v[0], v[1], v[2], v[3], [](float x, float y) { return fmax_nan(x, y); });
+      m = fold(v, [](float x, float y) { return fmax_nan(x, y); });
     }
     float s = 0;
     if (need_mass) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        // lane with pick = k
         const float top = __shfl_sync(~0u, m, (lane & 24) | (k >> 1) | (k & 1) << 1);
         const float ref = top == -kInf ? 0.0f : top;
         const Vec<ES> x(raw[k]);
@@ -898,16 +895,12 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
 #pragma unroll
         for (int e = 0; e < N; ++e) v[k] += weight_of(x.x[e], ref, R.sc);
       }
-      s = fold(v[0], v[1], v[2], v[3], [](float x, float y) { return x + y; });
+      s = fold(v, [](float x, float y) { return x + y; });
     }
-    if (!joined) {
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-      joined = true;
-    }
-    if ((lane & 4) == 0)
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
-                       stat0 + (i0 + pick * kThreads + lane) / 8 * 8),
-                   "f"(m), "f"(s)
+    join();
+    const int i = i0 + folded(lane) * kThreads + (lane & 24);  // the group's first vector
+    if ((lane & 4) == 0 && i < R.v1)
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(stat0 + i), "f"(m), "f"(s)
                    : "memory");
   };
   for (int i0 = i_first; i0 < R.v1; i0 += kThreads * Row<ES>::kLoads) {
@@ -915,7 +908,7 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
 #pragma unroll
     for (int k = 0; k < Row<ES>::kLoads; ++k) x[k] = ahead[k];
     if (i0 + kThreads * Row<ES>::kLoads < R.v1) R.fetch(i0 + kThreads * Row<ES>::kLoads, ahead);
-    if (G == 8 && R.whole(i0)) {
+    if (G == 8) {
       four(i0, x);
       continue;
     }
@@ -1131,7 +1124,8 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
   }
 
   // ---- the groups' kept masses, and the draw
-  R.each([&](int i, const uint4& raw) {
+  const uint32_t mass0 = peer_addr(&R.stat[0].y, 0);
+  auto kept = [&](int i, const uint4& raw) {
     const Vec<ES> x(raw);
     float s = 0;
 #pragma unroll
@@ -1140,11 +1134,30 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
       const bool on = (w >= min_p) & ((v > cut.t) | ((v == cut.t) & (R.token(i, e) <= cut.id)));
       s += on ? w : 0.0f;
     }
-    for (int d = 1; d < G; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
-    if ((lane & (G - 1)) == 0 && i < R.v1)
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(&R.stat[i >> a.shift].y, 0)), "f"(s)
-                   : "memory");
-  });
+    return s;
+  };
+  for (int i0 = R.start(); i0 < R.v1; i0 += kThreads * Row<ES>::kLoads) {
+    uint4 x[Row<ES>::kLoads];
+    float s[Row<ES>::kLoads];
+    R.fetch(i0, x);
+#pragma unroll
+    for (int k = 0; k < Row<ES>::kLoads; ++k) s[k] = kept(i0 + k * kThreads + lane, x[k]);
+    auto put = [&](int i, float v) {
+      if (i < R.v1)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mass0 + (i >> a.shift) * 8), "f"(v)
+                     : "memory");
+    };
+    if (G == 8) {
+      const float v = fold(s, [](float x, float y) { return x + y; });
+      if ((lane & 4) == 0) put(i0 + folded(lane) * kThreads + (lane & 24), v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < Row<ES>::kLoads; ++k) {
+        for (int d = 1; d < G; d <<= 1) s[k] += __shfl_xor_sync(~0u, s[k], d);
+        if ((lane & (G - 1)) == 0) put(i0 + k * kThreads + lane, s[k]);
+      }
+    }
+  }
   cluster_sync();
   if (rank == 0) draw<ES>(R, a, row, groups, u, cut, min_p);
 }
