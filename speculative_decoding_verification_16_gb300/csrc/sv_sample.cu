@@ -13,24 +13,30 @@
 //    are read again, and their tokens at or above it make a list.  If it holds
 //    the top-k set, or top_p of the mass, the row is finished on it: ranks by
 //    counting, the cuts, the draw.  This is the path of usual rows.
-//  - Otherwise (flat rows under top-p, top_k of hundreds, many ties) all CTAs of
-//    the row search: an interval of values around the cut is narrowed, three
-//    pivots a pass over the row (from L2), placed by interpolation, until it
-//    holds at most kList tokens, which are collected and ranked, or one value.
-//    Then one pass forms the groups' kept masses, and the draw is as without
-//    filters.
-// A pass of the search ends with an exchange: each CTA stores its partial into
-// every CTA's shared memory, and after the cluster barrier all sum the C
-// partials in rank order, so all decide alike.
+//  - Otherwise (flat rows under top-p, top_k of hundreds) all CTAs of the row count
+//    its tokens by weight in bins, collect the bin that the cut falls in and rank
+//    its tokens.  Then one pass forms the groups' kept masses, and the draw is as
+//    without filters.
+//  - A bin too full for a list (many ties, as in bf16) is searched: an interval of
+//    values around the cut is narrowed, three pivots a pass over the row, placed at
+//    the bin's edges and then by interpolation, until it holds at most kCollect
+//    tokens, which are collected and ranked, or one value, whose tokens are taken
+//    by ascending id.
+// A pass over the row after the first reads it from L2 and ends with an exchange:
+// each CTA stores its partial into every CTA's shared memory, and after the cluster
+// barrier all sum the C partials in rank order, so all decide alike.
 //
 // What bounds it.  One row: latency (151,936 bf16 under top-k 20 and top-p 0.95
-// 8.6 us: 1.3 us to the settings, 1.8 us for the row on eight SMs, 0.9 us of
+// 8.0 us: 1.3 us to the settings, 1.3 us for the row on eight SMs, 0.9 us of
 // cluster barriers, 3.5 us to decide).  Many rows: the stream at two CTAs an SM with
-// the decision's latency between (512 rows of 262,144 bf16, 268 MB: 86 us, 3.1 TB/s,
-// 0.47 of the measured copy rate).  Rows that need the search: instructions, about
-// three passes over the row (96 flat fp32 rows of 129,280 under top-p 96 us).
+// the decision's latency between, and 512 rows are 1.7 times what fits (512 rows of
+// 262,144 bf16, 268 MB: 65 us, 4.1 TB/s, 0.62 of the measured copy rate; four CTAs of
+// 256 threads an SM 61 us, but 32 rows with their own settings 66 us against 32).
+// Rows whose cut needs the bins: instructions, four passes over the row (96 flat
+// fp32 rows of 129,280 under top-p 80 us).
 // Rows held in the cluster's shared memory instead of read again measured slower:
-// 180 us for the 512 rows, the resident bytes waiting through every decision.
+// 180 us for the 512 rows where reading again took 86, the resident bytes waiting
+// through every decision.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -47,7 +53,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;      // most tokens of a list
-constexpr int kCollect = 256;   // most tokens that a search collects
+constexpr int kCollect = 512;   // most tokens that a search collects
 constexpr int kBins = 2048;     // of 1/64 binade of weight
 constexpr int kTopPSeeds = 192;  // group maxima that a top-p row's bar lies below
 constexpr float kInf = __builtin_huge_valf();
@@ -73,7 +79,7 @@ struct Header {
       float w[kList];       // rank 0: weights and ids, best first
       int32_t id[kList];
     };
-    int32_t bins[kBins];  // counts of tokens by weight
+    uint32_t bins[kBins];  // tokens by weight
   };
   uint64_t list[kCollect];  // this CTA's part of what a search collects
   uint64_t sum[kWarps];
@@ -385,27 +391,34 @@ struct Cut {
   float mass;
   int parity = 0;   // of the row's next exchange
   bool ok = true;
+  float lo = kInf, hi = -kInf;  // not ok: values that the cut probably lies between, if lo <= hi
 };
 
 // The cut at the k-th best token (need < 0), or where the mass reaches `need`,
 // among the tokens up to `within`: the tokens below top_x counted by 1/64 binade
-// of weight (one pass), the bins around the cut collected and ranked (another).
+// of weight (one pass; each counts as its weight relative to the bin's middle, in
+// whole 2^-12; with plain counts one row in ten missed the bin and took the search:
+// 96 flat rows of 151,936 bf16 132 us, 80 now), the bins around the cut collected and
+// ranked (another).
 // Tokens at or above top_x (infinite: none) number c_top, with mass m_top; the
 // cut does not lie below floor_x.  The
-// bins' masses are estimates (count times middle weight), the masses that decide
+// bins' masses are estimates, the masses that decide
 // are sums; not ok if the cut lies outside what was collected.
 template <int ES>
 __device__ __noinline__ Cut cut_by_bins(Row<ES> R, int k, float need, Cut within, float top_x,
                                         float m_top, int c_top, float floor_x) {
   constexpr int N = 16 / ES, kPer = kBins / kThreads;
+  constexpr uint32_t kUnit = 4096;             // a token of its bin's middle weight
+  constexpr float kSlope = 0.01083042469625f;  // log(2) / 64: a bin's width in the weights
+  static_assert(SV_SAMPLE_MAX_ROW_BYTES / 2 * (kUnit * 1.006) < 4294967295.0, "a bin's sum");
   const bool by_mass = need >= 0.0f;
   Header* h = R.h;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float origin = top_x < kInf ? top_x : R.best, step = fminf(R.sc * 64.0f, 3.0e38f);
   // rounded to the nearest by an addition (conversions run at a quarter of its rate)
+  auto bin_at = [&](float x) { return fminf((origin - x) * step, kBins - 1.0f); };
   auto bin_of = [&](float x) {
-    return __float_as_int(fminf(fmaf(origin - x, step, 0x1p23f), 0x1p23f + (kBins - 1))) -
-           __float_as_int(0x1p23f);
+    return __float_as_int(bin_at(x) + 0x1p23f) - __float_as_int(0x1p23f);
   };
   const float low = fmaxf(fmaxf(floor_x, within.t), -3.4028235e38f);
   // of tokens at within.t only some may count; NaN: all do
@@ -419,29 +432,38 @@ __device__ __noinline__ Cut cut_by_bins(Row<ES> R, int k, float need, Cut within
     const Vec<ES> x(raw);
 #pragma unroll
     for (int e = 0; e < N; ++e)
-      if (inside(x.x[e], R.token(i, e))) atomicAdd(&h->bins[bin_of(x.x[e])], 1);
+      if (inside(x.x[e], R.token(i, e))) {
+        const float y = bin_at(x.x[e]), near = y + 0x1p23f, off = y - (near - 0x1p23f);
+        const uint32_t w = by_mass ? __float_as_uint(fmaf(off, -kSlope * kUnit, 0x1p23f + kUnit)) -
+                                         __float_as_uint(0x1p23f)
+                                   : kUnit;
+        atomicAdd(&h->bins[__float_as_int(near) - __float_as_int(0x1p23f)], w);
+      }
   });
   cluster_sync();
-  int first = 0, end = 0;  // bins to collect
+  int first = 0, end = 0, at_bin = 0;  // bins to collect; the cut's
   if (R.rank == 0) {
     static_assert(kPer == 4, "one 16-byte load a thread and rank");
-    int4 x[kMaxCluster];
+    uint4 x[kMaxCluster];
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
       if (r < R.C)
-        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(x[r].x), "=r"(x[r].y), "=r"(x[r].z), "=r"(x[r].w)
                      : "r"(peer_addr(&h->bins[tid * kPer], r)));
-    int n[kPer] = {0, 0, 0, 0};
+    uint32_t units[kPer] = {0, 0, 0, 0};
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
-      if (r < R.C) n[0] += x[r].x, n[1] += x[r].y, n[2] += x[r].z, n[3] += x[r].w;
-    const float w0 = R.weight(origin);
+      if (r < R.C)
+        units[0] += x[r].x, units[1] += x[r].y, units[2] += x[r].z, units[3] += x[r].w;
+    const float w0 = R.weight(origin) * (1.0f / kUnit);
+    int n[kPer];
     float mass[kPer], m = 0;
     int c = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      mass[j] = static_cast<float>(n[j]) * w0 * ex2(-(tid * kPer + j) / 64.0f);
+      n[j] = static_cast<int>((units[j] + kUnit / 2) / kUnit);
+      mass[j] = static_cast<float>(units[j]) * w0 * ex2(-(tid * kPer + j) / 64.0f);
       m += mass[j], c += n[j];
     }
     float mi = m;
@@ -461,35 +483,55 @@ __device__ __noinline__ Cut cut_by_bins(Row<ES> R, int k, float need, Cut within
     mi += m_top, ci += c_top;
     for (int w = 0; w < warp; ++w) mi += h->part[w][0].x, ci += __float_as_int(h->part[w][0].y);
     mi -= m, ci -= c;  // before this thread's bins
+    int at = kBins;
+    float past = 0.5f;  // how much of the bin lies past the cut
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       mi += mass[j], ci += n[j];
       if (n[j] > 0 && (by_mass ? mi >= need : ci >= k)) {
-        atomicMin(&h->cut, tid * kPer + j);
+        at = tid * kPer + j;
+        if (by_mass) past = (mi - need) / mass[j];
         break;
       }
     }
+    if (at < kBins) atomicMin(&h->cut, at);
+    __syncthreads();
+    if (at < kBins && at == h->cut) h->base = past;
     __syncthreads();
     if (tid == 0) {  // the cut's bin and its neighbours, while a list holds them
-      int b = h->cut, lo = b, hi = b + 1, total = b < kBins - 1 ? h->bins[b] : kCollect + 1;
-      for (int j = 0; j < 4 && total <= kCollect; ++j) {
-        if (hi < kBins - 1 && total + h->bins[hi] <= kCollect) total += h->bins[hi++];
-        if (lo > 0 && total + h->bins[lo - 1] <= kCollect) total += h->bins[--lo];
+      constexpr int kMost = kCollect - 4, kFew = kCollect / 2;  // counts are off by half a percent
+      int b = h->cut, lo = b, hi = b + 1;
+      int total = b < kBins - 1 ? static_cast<int>(h->bins[b]) : kCollect;
+      auto fits = [&](int i, int most) {
+        return i >= 0 && i < kBins - 1 && total + static_cast<int>(h->bins[i]) <= most;
+      };
+      // near an edge of the bin the cut may lie in the next
+      if (h->base < 0.0625f && fits(hi, kMost)) total += h->bins[hi++];
+      if (h->base > 0.9375f && fits(lo - 1, kMost)) total += h->bins[--lo];
+      for (int j = 0; j < 4; ++j) {
+        if (fits(hi, kFew)) total += h->bins[hi++];
+        if (fits(lo - 1, kFew)) total += h->bins[--lo];
       }
-      if (total > kCollect) lo = hi = 0;
+      if (total > kMost) lo = hi = 0;
       h->group = lo, h->groups = hi;
     }
     __syncthreads();
-    first = h->group, end = h->groups;
+    first = h->group, end = h->groups, at_bin = h->cut;
   }
   __syncthreads();
   if (tid == 0) h->count = 0;
   {
-    const float4(*s)[2] = R.exchange(make_float4(__int_as_float(first), __int_as_float(end), 0, 0),
-                                     make_float4(0, 0, 0, 0));
+    const float4(*s)[2] = R.exchange(
+        make_float4(__int_as_float(first), __int_as_float(end), __int_as_float(at_bin), 0),
+        make_float4(0, 0, 0, 0));
     first = __float_as_int(s[0][0].x), end = __float_as_int(s[0][0].y);
+    at_bin = __float_as_int(s[0][0].z);
   }
   Cut cut{0.0f, -1, 0.0f, R.parity, false};
+  if (at_bin < kBins - 1) {  // for the search
+    const float wide = end == 0 ? 0.5f : 3.0f;
+    cut.lo = origin - (at_bin + wide) / step, cut.hi = origin - (at_bin - wide) / step;
+  }
   if (end == 0) return cut;
   typename Row<ES>::Sums v{{0, 0, 0}, {0, 0, 0}};  // mass and count above the collected bins
   R.each([&](int i, const uint4& raw) {
@@ -539,13 +581,19 @@ __device__ __noinline__ Cut cut_by_bins(Row<ES> R, int k, float need, Cut within
 // tokens, or less mass than need, at or above it, their count and mass.
 template <int ES>
 __device__ __noinline__ Cut search(Row<ES> R, int k, float need, uint32_t lo, int lo_id,
-                                   float m_lo, int c_lo, uint32_t hi, float m_hi, int c_hi) {
+                                   float m_lo, int c_lo, uint32_t hi, float m_hi, int c_hi,
+                                   float guess_lo, float guess_hi) {
   const bool by_mass = need >= 0.0f;
   constexpr uint32_t kLow = ES == 2 ? 0x7fu : 0x7fffffu;  // key of -inf
   for (int iter = 0; hi - lo > 1 && c_lo - c_hi > kCollect; ++iter) {
     const float xh = fminf(float_of<ES>(hi), R.best), xl = float_of<ES>(lo);
     uint32_t p[3];
-    if (iter < 8 && lo == kLow) {  // no lower end yet: steps of some binades of weight
+    if (iter == 0 && guess_lo <= guess_hi) {
+      // a bin too full for a list; in bf16 often one value: the two keys around it
+      p[0] = key_of<ES>(guess_lo), p[2] = key_of<ES>(guess_hi) + 1;
+      if (float_of<ES>(p[0]) < guess_lo && p[0] + 1 < p[2]) ++p[0];
+      p[1] = p[0] + (p[2] - p[0]) / 2;
+    } else if (iter < 8 && lo == kLow) {  // no lower end yet: steps of some binades of weight
       const float unit = 1.0f / R.sc;
 #pragma unroll
       for (int j = 0; j < 3; ++j)
@@ -1108,7 +1156,8 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
     cut = cut_by_bins<ES>(R, top_k, need, all, below ? bar_x : kInf, m_top, c_top, floor_x);
     R.parity = cut.parity;
     if (!cut.ok) {
-      cut = search<ES>(R, top_k, need, kLow, -1, row_mass, a.V, below ? bar_key : above, m_top, c_top);
+      cut = search<ES>(R, top_k, need, kLow, -1, row_mass, a.V, below ? bar_key : above, m_top, c_top,
+                       cut.lo, cut.hi);
       R.parity = cut.parity;
     }
   }
@@ -1118,7 +1167,8 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
     cut = cut_by_bins<ES>(R, 0, need, k, kInf, 0.0f, 0, -kInf);
     R.parity = cut.parity;
     if (!cut.ok) {
-      cut = search<ES>(R, 0, need, key_of<ES>(k.t), k.id, k.mass, INT32_MAX, above, 0.0f, 0);
+      cut = search<ES>(R, 0, need, key_of<ES>(k.t), k.id, k.mass, INT32_MAX, above, 0.0f, 0,
+                       cut.lo, cut.hi);
       R.parity = cut.parity;
     }
   }
@@ -1190,8 +1240,8 @@ extern "C" int spec_verify_sample(const void* logits, int64_t row_stride, int32_
   const int per = 16 / es, vecs = (V + per - 1) / per + 1;  // one more where the row starts between
   // CTAs a row, each of at least 512 vectors: one an SM for up to a quarter as
   // many rows as SMs (the kernel then has 128 registers a thread; 32 rows under
-  // top-p 48 us, two an SM 55 us), else as many as fit at two an SM (96 rows:
-  // three CTAs a row 15 us, four 24 us; 512 rows: one 59 us, two 72 us).
+  // top-p 0.8 48 us, two an SM 52 us), else as many as fit at two an SM (96 rows under top-k 20:
+  // three CTAs a row 12 us, four 20 us).
   const bool wide = 4 * static_cast<int64_t>(N) <= d.sms;
   const int C = std::max(1, std::min({kMaxCluster, (wide ? 1 : 2) * d.sms / N, vecs / 512}));
   if (static_cast<int64_t>(N) * C > INT32_MAX) return SV_ERR_UNSUPPORTED;
