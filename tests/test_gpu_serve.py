@@ -96,6 +96,21 @@ def test_sample_ties_zeros_and_masks(cuda_lib, dtype, V):
         check_sample(cuda_lib, xt, rng.random(N), None, [k] * N, [p] * N, [m] * N)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [0.05, 1.3, 60.0])
+@pytest.mark.parametrize("V", [5001, 60000])
+def test_sample_flat_rows(cuda_lib, dtype, T, V):
+    """Cuts far down flat rows: among few and among thousands of tokens of about one
+    weight, the row longer than a CTA's part by a few tokens."""
+    rng = np.random.default_rng(V)
+    N = 72
+    x = torch.tensor(rng.normal(0, 3, (N, V)), dtype=dtype, device=DEV)
+    p = rng.uniform(0.3, 0.995, N)
+    k = np.where(np.arange(N) % 3 == 0, rng.integers(200, V, N), 0)
+    check_sample(cuda_lib, x, rng.random(N), [T] * N, k, np.where(np.arange(N) % 6 == 0, 1.0, p),
+                 np.where(np.arange(N) % 4 == 0, 0.001, 0.0), V + 7)
+
+
 def test_sample_without_settings_and_extremes(cuda_lib):
     rng = np.random.default_rng(3)
     x = torch.tensor(rng.normal(0, 2, (5, 5003)), dtype=F32, device=DEV)
