@@ -1089,11 +1089,13 @@ __global__ __launch_bounds__(kThreads, PER_SM) void sample_kernel(const SampleAr
             if (use_k) R.reach(keep, kInf, &kept);
             total = kept;
             if (use_p) keep = R.reach(keep, top_p * kept, &total);
-            if (min_p > 0.0f) {
+            // below the bar of min-p, or of no weight (masked, or 2^y underflowed): the
+            // sums' rounding may leave the target at their mass, and draw none of them
+            if (min_p > 0.0f || !(h->w[keep - 1] > 0.0f)) {
               int c = 0;
-              for (int i = lane; i < keep; i += 32) c += h->w[i] >= min_p ? 1 : 0;
+              for (int i = lane; i < keep; i += 32) c += h->w[i] > 0.0f && h->w[i] >= min_p ? 1 : 0;
               keep = __reduce_add_sync(~0u, c);
-              R.reach(keep, kInf, &total);
+              if (min_p > 0.0f) R.reach(keep, kInf, &total);
             }
             if (lane == 0) h->cut = keep, h->total = total, h->pick = INT32_MAX;
           }
