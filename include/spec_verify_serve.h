@@ -86,7 +86,8 @@ int spec_verify_sample(const void* logits, int64_t row_stride, int32_t N, int32_
  *  free_count      [1] int32 device: ids on the stack before the call.
  *  n_rows          rows of positions and slots; at least the sum of verify_lens.
  *  out_row_offsets [B+1] int32: prefix sums of verify_lens.
- *  out_seq_lens    [B] int32: context + new.
+ *  out_seq_lens    [B] int32: context + new; -1 for a request that is not served
+ *                  or out of range (below).
  *  out_positions   [n_rows] int32: position of every new token in its request;
  *                  0 in the rows past the last token.
  *  out_slots       [n_rows] int64: page * page_size + offset; -1 in those rows.
@@ -98,7 +99,10 @@ int spec_verify_sample(const void* logits, int64_t row_stride, int32_t N, int32_
  * is not keeps what it holds and its tokens past those pages get slot -1.  A
  * request with a negative length, more pages than width or a held count
  * outside [0, width] (SV_DEVERR_LEN) keeps its pages and its slots are -1;
- * a verify_lens outside [0, n_rows] counts as no rows.
+ * a verify_lens outside [0, n_rows] counts as no rows.  The tables of both kinds
+ * do not hold their tokens' pages (entries past the held ones may name pages of
+ * other requests), so their out_seq_lens is -1, which spec_verify_attention
+ * refuses for the request alone: the step may run on before the flags are read.
  */
 int spec_verify_slots(const int32_t* context_lens, const int32_t* verify_lens, int32_t B,
                       int32_t page_size, int32_t* block_table, int64_t table_stride,
@@ -139,10 +143,12 @@ int spec_verify_append(const void* key, const void* value, int64_t k_row_stride,
  *  query        [n_rows][heads][head_dim]; strides multiples of 16 bytes.
  *  caches       as in spec_verify_append; base and strides multiples of 16 bytes.
  *  block_table  [B][table_stride >= table_width] int32 device.  A page id
- *               outside [0, num_blocks) raises SV_DEVERR_PAGE; a seq_len past
- *               table_width * page_size or row_offsets that do not rise within
- *               [0, n_rows] raise SV_DEVERR_LEN and the request is left out.
- *  max_len      host upper bound of every l (SV_DEVERR_LEN if exceeded).
+ *               outside [0, num_blocks) raises SV_DEVERR_PAGE; a seq_len below 0
+ *               or past table_width * page_size, or more rows than max_len, raise
+ *               SV_DEVERR_LEN and the request's rows see no key; row_offsets that
+ *               do not rise within [0, n_rows] raise it and the request's rows
+ *               are not written.
+ *  max_len      host upper bound of every l.
  *  head_dim     a multiple of 8, up to SV_ATTN_MAX_HEAD_DIM; heads a multiple
  *               of kv_heads.
  *  scale        factor of the scores, finite.

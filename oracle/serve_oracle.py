@@ -85,8 +85,11 @@ def slots(ctx, new, table, held, free, count, page, n_rows):
             pos[offs[r] + i] = p
             if p // page < held_out[r]:
                 slot[offs[r] + i] = int(table[r, p // page]) * page + p % page
+    # no length for a request whose pages do not hold its tokens
+    seq = [int(ctx[r]) + int(new[r]) if need[r] is not None and held_out[r] == need[r] else -1
+           for r in range(B)]
     return dict(table=table, stack=stack, count=len(free), held=held_out, row_offsets=offs,
-                seq_lens=np.asarray(ctx) + np.asarray(new), positions=pos, slots=slot, errors=err)
+                seq_lens=seq, positions=pos, slots=slot, errors=err)
 
 
 def attention_request(q, k, v, scale, window=0):

@@ -35,18 +35,23 @@ struct AttnArgs {
   FastDiv by_group, by_page;
 };
 
-// Request r's rows and length, or l = -1 when they are out of range.
+// Request r's rows and length.  Rows out of range: l = -1.  A length out of range,
+// or more rows than max_len: no key is seen, so that the rows become zeros.  *bad is
+// raised for both.
 struct Span {
   int32_t row0, l, seq;
 };
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int r) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int r, bool* bad = nullptr) {
   Span s;
   s.row0 = a.row_offsets[r];
   const int32_t end = a.row_offsets[r + 1];
   s.seq = a.seq_lens[r];
-  const bool ok = s.row0 >= 0 && end >= s.row0 && end <= a.n_rows && end - s.row0 <= a.max_len &&
-                  s.seq >= 0 && s.seq <= static_cast<int64_t>(a.table_width) * a.page;
-  s.l = ok ? end - s.row0 : -1;
+  const bool rows = s.row0 >= 0 && end >= s.row0 && end <= a.n_rows;
+  const bool keys = rows && end - s.row0 <= a.max_len && s.seq >= 0 &&
+                    s.seq <= static_cast<int64_t>(a.table_width) * a.page;
+  s.l = rows ? end - s.row0 : -1;
+  if (!keys) s.seq = 0;
+  if (bad != nullptr) *bad |= !keys;
   return s;
 }
 

@@ -179,8 +179,7 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
   int64_t mine = 0, per_head = 0;
   bool bad = false;
   for (int r = tid; r < a.B; r += THREADS) {
-    s = span_of(a, r);
-    bad |= s.l < 0;
+    s = span_of(a, r, &bad);
     per_head = head_tiles<MR>(p, s);
     mine += per_head;
   }

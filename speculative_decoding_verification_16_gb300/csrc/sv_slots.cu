@@ -153,9 +153,8 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
       s2 = max(q.need - q.held, 0);
       if (!q.ok) err |= SV_DEVERR_LEN;
       ctxs[r] = q.ctx, keep[r] = q.ok ? q.held : -1;
-      if (first)
-        a.seq_lens[r] = static_cast<int32_t>(
-            min(static_cast<int64_t>(q.ctx) + q.fresh, static_cast<int64_t>(INT32_MAX)));
+      // -1: attention leaves the request out; its table does not hold its tokens' pages
+      if (first) a.seq_lens[r] = q.ok ? q.ctx + q.fresh : -1;
     }
     const int64_t own0 = s0;
     const int32_t own1 = s1, own2 = s2;
@@ -205,7 +204,7 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
     for (int r = tid; r < a.B; r += kSlotThreads) {
       const int32_t taken = take[r + 1] - take[r];
       const bool served = take[r + 1] <= avail || taken == 0;
-      if (!served) err |= SV_DEVERR_BLOCKS;
+      if (!served) err |= SV_DEVERR_BLOCKS, a.seq_lens[r] = -1;  // over this thread's own store
       a.held_out[r] = keep[r] < 0 ? a.held[r]
                                   : keep[r] + (served ? taken : 0) - (give[r + 1] - give[r]);
     }

@@ -37,3 +37,70 @@ def test_tokens_without_weight_are_never_drawn(cuda_lib, dtype, V):
                                                 want_probs=True)
         assert (xt.gather(1, tok.long()[:, None]) >= 0).all()
         assert (prob > 0).all()
+
+
+# ---------------------------------------------------------------- shortage
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_request_without_pages_reads_no_other_requests_cache(cuda_lib, dtype):
+    """Three requests want pages, the second finds none.  Its table still holds ids
+    of pages that others own; its rows come out as zeros, flagged, and the others'
+    rows as they are without it."""
+    lib = cuda_lib
+    page, H, D = 16, 2, 64
+    g = torch.Generator(device=DEV).manual_seed(0)
+    kc, vc = (torch.randn(8, page, H, D, device=DEV, generator=g).to(dtype) for _ in range(2))
+    q, k, v = (torch.randn(9, H, D, device=DEV, generator=g).to(dtype) for _ in range(3))
+    # request 1 holds page 5; its row's next entries are pages that it gave back long ago
+    table = i32([[1, 2, 0, 0], [5, 1, 2, 3], [3, 4, 0, 0]])
+    err = dev_error()
+    plan = lib.spec_verify_slots(i32([20, 15, 18]), i32([3, 40, 2]), table, i32([2, 1, 2]),
+                                 i32([6, 0]), i32([1]), page_size=page, n_rows=48, dev_error=err)
+    assert err.item() == lib.SV_DEVERR_BLOCKS
+    assert plan.seq_lens.tolist() == [23, -1, 20]
+    plan = lib.spec_verify_slots(i32([20, 15, 18]), i32([3, 4, 2]), table, i32([2, 1, 2]),
+                                 i32([6, 0]), i32([0]), page_size=page, n_rows=9, dev_error=err)
+    assert plan.seq_lens.tolist() == [23, -1, 20] and plan.held.tolist() == [2, 1, 2]
+    err.zero_()
+    lib.spec_verify_append(k, v, plan.slots, kc, vc, dev_error=err)
+    out = torch.full((9, H, D), 7.0, device=DEV, dtype=dtype)
+    lse = torch.full((9, H), 7.0, device=DEV)
+    lib.spec_verify_attention(q, kc, vc, table, plan.seq_lens, plan.row_offsets, max_len=4, out=out,
+                              lse=lse, dev_error=err)
+    assert err.item() == lib.SV_DEVERR_LEN
+    assert (out[3:7] == 0).all() and (lse[3:7] == -float("inf")).all()
+    rest = torch.cat([q[:3], q[7:]])
+    want, wl = lib.spec_verify_attention(rest, kc, vc, table[[0, 2]], i32([23, 20]), i32([0, 3, 5]),
+                                         max_len=4, want_lse=True)
+    assert torch.equal(torch.cat([out[:3], out[7:]]), want)
+    assert torch.equal(torch.cat([lse[:3], lse[7:]]), wl)
+
+
+def test_requests_out_of_range_get_no_length(cuda_lib):
+    """A negative context, more pages than the table has columns, a count of pages
+    outside it: the length that comes out is one that attention refuses."""
+    lib, err = cuda_lib, dev_error()
+    out = lib.spec_verify_slots(i32([-1, 5, 3, 2, 3]), i32([2, 20, 1, -4, 0]),
+                                i32(np.arange(20).reshape(5, 4)), i32([1, 2, 1, 9, 1]),
+                                i32([90, 91, 92]), i32([3]), page_size=4, n_rows=30, dev_error=err)
+    assert err.item() == lib.SV_DEVERR_LEN
+    assert out.seq_lens.tolist() == [-1, -1, 4, -1, 3]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_of_a_request_that_is_left_out_are_zeros(cuda_lib, dtype):
+    kc = torch.randn(4, 16, 1, 64, device=DEV).to(dtype)
+    q = torch.randn(6, 2, 64, device=DEV).to(dtype)
+    ok, okl = cuda_lib.spec_verify_attention(q, kc, kc.clone(), i32([[0, 1], [2, 3]]), i32([20, 30]),
+                                             i32([0, 3, 6]), max_len=3, want_lse=True)
+    for seq, offs, max_len in (([20, 33], [0, 3, 6], 3), ([20, -1], [0, 3, 6], 3),
+                               ([20, 30], [0, 2, 6], 3)):
+        err = dev_error()
+        out, lse = torch.full_like(q, 9.0), torch.full((6, 2), 9.0, device=DEV)
+        cuda_lib.spec_verify_attention(q, kc, kc.clone(), i32([[0, 1], [2, 3]]), i32(seq), i32(offs),
+                                       max_len=max_len, out=out, lse=lse, dev_error=err)
+        assert err.item() == cuda_lib.SV_DEVERR_LEN
+        n = offs[1]
+        assert (out[n:] == 0).all() and (lse[n:] == -float("inf")).all()
+        if n == 3:
+            assert torch.equal(out[:3], ok[:3]) and torch.equal(lse[:3], okl[:3])
