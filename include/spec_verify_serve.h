@@ -92,9 +92,11 @@ int spec_verify_sample(const void* logits, int64_t row_stride, int32_t N, int32_
  *                  0 in the rows past the last token.
  *  out_slots       [n_rows] int64: page * page_size + offset; -1 in those rows.
  *  out_held        [B] int32 and out_free_count [1] int32: the counts after the
- *                  call.  They must not be the arrays of the counts before it
- *                  (the kernel reads those throughout): a caller keeps two and
- *                  takes them in turn.
+ *                  call.
+ * No result may overlap context_lens, verify_lens, held or free_count (the kernel
+ * reads those throughout; SV_ERR_ARG): a caller keeps two arrays of each count
+ * and takes them in turn.
+ *
  * Requests are served in order while pages last (SV_DEVERR_BLOCKS): one that
  * is not keeps what it holds and its tokens past those pages get slot -1.  A
  * request with a negative length, more pages than width or a held count

@@ -449,8 +449,8 @@ def spec_verify_slots(context_lens, verify_lens, block_table, held, free_list, f
     """Block tables and slot maps of a step.  ``block_table`` [B, width] and
     ``free_list`` are updated in place so that every request holds exactly the
     pages of its context and new tokens; ``held`` [B] and ``free_count`` [1]
-    are the counts before the call and are returned anew (``held_out`` and
-    ``free_count_out`` must be other tensors).  Returns SlotOutputs: prefix
+    are the counts before the call and are returned anew.  No result may share
+    memory with them, ``context_lens`` or ``verify_lens``.  Returns SlotOutputs: prefix
     sums of verify_lens [B + 1], sequence lengths [B], and for ``n_rows`` rows
     (at least the sum of verify_lens; the length of ``slots`` if given) the
     positions int32 and slots int64."""

@@ -344,7 +344,20 @@ int spec_verify_slots(const int32_t* context_lens, const int32_t* verify_lens, i
     return SV_ERR_ARG;
   if (n_rows > 0 && (out_positions == nullptr || out_slots == nullptr)) return SV_ERR_ARG;
   if (!aligned_to(out_positions, 4) || !aligned_to(out_slots, 8)) return SV_ERR_ARG;
-  if (out_held == held || out_free_count == free_count) return SV_ERR_ARG;
+  // CTAs read these while others write the results
+  const struct {
+    const void* at;
+    int64_t bytes;
+  } in[] = {{context_lens, 4 * int64_t{B}}, {verify_lens, 4 * int64_t{B}},
+            {held, 4 * int64_t{B}}, {free_count, 4}},
+    results[] = {{out_row_offsets, 4 * (int64_t{B} + 1)}, {out_seq_lens, 4 * int64_t{B}},
+                 {out_positions, 4 * int64_t{n_rows}}, {out_slots, 8 * int64_t{n_rows}},
+                 {out_held, 4 * int64_t{B}}, {out_free_count, 4}};
+  for (const auto& o : results)
+    for (const auto& i : in)
+      if (o.bytes > 0 && static_cast<const char*>(o.at) < static_cast<const char*>(i.at) + i.bytes &&
+          static_cast<const char*>(i.at) < static_cast<const char*>(o.at) + o.bytes)
+        return SV_ERR_ARG;
   sv::serve::Device d;
   const int rc = sv::serve::device(&d);
   if (rc != SV_OK) return rc;

@@ -2,6 +2,7 @@
 entries refuse and accept without touching a device."""
 
 import numpy as np
+import pytest
 
 from oracle import serve_oracle as S
 
@@ -12,3 +13,32 @@ def test_slots_oracle_gives_unserved_requests_no_length():
                   np.array([4, 5]), 2, 4, 20)
     assert got["errors"] == {"blocks", "len"} and got["held"] == [1, 0, 1, 0]
     assert got["seq_lens"] == [4, -1, 4, -1]
+
+
+# ---------------------------------------------------------------- refusals
+
+P = 1 << 20  # aligned addresses a megabyte apart, never dereferenced
+ERR_ARG = -1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from speculative_decoding_verification_16_gb300 import build
+    build.build()
+    from speculative_decoding_verification_16_gb300 import binding
+    return binding._lib
+
+
+SLOTS = dict(ctx=P, new=2 * P, B=4, page=16, table=3 * P, stride=8, width=8, held=4 * P,
+             free=5 * P, cap=64, count=6 * P, rows=10, offs=7 * P, seq=8 * P, pos=9 * P,
+             slots=10 * P, held_out=11 * P, count_out=12 * P, err=13 * P, stream=None)
+
+
+@pytest.mark.parametrize("result", ["offs", "seq", "pos", "slots", "held_out", "count_out"])
+@pytest.mark.parametrize("read", ["ctx", "new", "held", "count"])
+def test_slots_refuses_results_over_what_it_reads(lib, result, read):
+    """CTAs read the lengths and counts while others write the results."""
+    for shift in (0, 8 if result == "slots" else 4):  # the same place, and one in part
+        last = dict(offs=16, seq=12, pos=36, slots=72, held_out=12, count_out=0)[result]
+        a = {**SLOTS, result: SLOTS[read] - (last if shift else 0)}
+        assert lib.spec_verify_slots(*a.values()) == ERR_ARG
