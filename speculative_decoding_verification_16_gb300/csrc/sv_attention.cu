@@ -254,6 +254,7 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
   if (static_cast<int64_t>(table_width) * page_size > INT32_MAX / 2 ||
       static_cast<int64_t>(n_rows) * heads > INT32_MAX)
     return SV_ERR_UNSUPPORTED;
+  if (n_rows == 0) return SV_OK;  // an empty tensor has no address
   if (query == nullptr || key_cache == nullptr || value_cache == nullptr || out == nullptr ||
       block_table == nullptr || seq_lens == nullptr || row_offsets == nullptr)
     return SV_ERR_ARG;
@@ -271,7 +272,6 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
   if (workspace == nullptr || !aligned_to(workspace, 256) ||
       workspace_bytes < spec_verify_attention_workspace_size(n_rows, heads, head_dim, dtype))
     return SV_ERR_WORKSPACE;
-  if (n_rows == 0) return SV_OK;
   const float c = scale * kLog2e;
   const AttnArgs a{static_cast<const char*>(query), q_row_stride * es, q_head_stride * es,
                    static_cast<const char*>(key_cache), static_cast<const char*>(value_cache),

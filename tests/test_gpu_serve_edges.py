@@ -104,3 +104,15 @@ def test_rows_of_a_request_that_is_left_out_are_zeros(cuda_lib, dtype):
         assert (out[n:] == 0).all() and (lse[n:] == -float("inf")).all()
         if n == 3:
             assert torch.equal(out[:3], ok[:3]) and torch.equal(lse[:3], okl[:3])
+
+
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_without_rows(cuda_lib, dtype):
+    """A step in which no request has new tokens."""
+    kc = torch.randn(4, 16, 2, 64, device=DEV).to(dtype)
+    q = torch.empty(0, 4, 64, dtype=dtype, device=DEV)
+    out, lse = cuda_lib.spec_verify_attention(q, kc, kc.clone(), i32([[0, 1], [2, 3]]), i32([20, 30]),
+                                              i32([0, 0, 0]), max_len=1, want_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)

@@ -1,6 +1,8 @@
 """Host side of the paged serving operators (no GPU): pins of the oracle, what the C
 entries refuse and accept without touching a device."""
 
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -42,3 +44,11 @@ def test_slots_refuses_results_over_what_it_reads(lib, result, read):
         last = dict(offs=16, seq=12, pos=36, slots=72, held_out=12, count_out=0)[result]
         a = {**SLOTS, result: SLOTS[read] - (last if shift else 0)}
         assert lib.spec_verify_slots(*a.values()) == ERR_ARG
+
+
+def test_attention_without_rows_needs_no_rows_memory(lib):
+    """An empty tensor has no address: a step without new tokens is no error."""
+    ok = lib.spec_verify_attention(None, 1024, 128, P, P, 16384, 1024, 128, P, 8, 8, P, P, 4, 0, 4,
+                                   8, 8, 128, 9, 16, 0, ctypes.c_float(0.1), 0, None, 1024, 128,
+                                   None, None, P, 1 << 40, None)
+    assert ok == 0
