@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -272,13 +273,16 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
   if (workspace == nullptr || !aligned_to(workspace, 256) ||
       workspace_bytes < spec_verify_attention_workspace_size(n_rows, heads, head_dim, dtype))
     return SV_ERR_WORKSPACE;
-  const float c = scale * kLog2e;
+  // the largest scales leave fp32 here: inf * 0 would be NaN where the score is 0
+  const float c = std::min(std::max(scale * kLog2e, -FLT_MAX), FLT_MAX);
   const AttnArgs a{static_cast<const char*>(query), q_row_stride * es, q_head_stride * es,
                    static_cast<const char*>(key_cache), static_cast<const char*>(value_cache),
                    block_stride * es, token_stride * es, head_stride * es, block_table,
                    table_stride, table_width, seq_lens, row_offsets, B, n_rows, max_len, heads,
                    heads / kv_heads, head_dim, num_blocks, page_size, window,
-                   c == 0.0f ? 1e-37f : c,  // masked scores stay -inf
+                   // scale 0: masked scores stay -inf, and no finite product weighs: 2^128 2^-149
+                   // is nothing beside 1
+                   c == 0.0f ? 0x1p-149f : c,
                    static_cast<char*>(out), o_row_stride * es, o_head_stride * es, out_lse,
                    dev_error, FastDiv::by(static_cast<uint32_t>(heads / kv_heads)),
                    FastDiv::by(static_cast<uint32_t>(page_size))};

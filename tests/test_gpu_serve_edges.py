@@ -116,3 +116,85 @@ def test_attention_without_rows(cuda_lib, dtype):
     out, lse = cuda_lib.spec_verify_attention(q, kc, kc.clone(), i32([[0, 1], [2, 3]]), i32([20, 30]),
                                               i32([0, 0, 0]), max_len=1, want_lse=True)
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("scale", [0.0, -0.125])
+def test_attention_signs_of_the_scale(cuda_lib, dtype, D, scale):
+    """Requests cut into parts, tiles on the causal edge, chunks; the scores are no
+    larger than at the default scale, so the same bounds hold."""
+    check_attention(cuda_lib, dtype, [(9001, 16), (700, 5), (37, 1), (0, 2)], 2, 4, D, 16,
+                    scale=scale * (64 / D) ** 0.5)
+    check_attention(cuda_lib, dtype, [(700, 300), (257, 257)], 1, 2, D, 64, window=200,
+                    scale=scale * (64 / D) ** 0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [6.0, -6.0])
+@pytest.mark.parametrize("lens,G", [([(9001, 16), (700, 5), (37, 1)], 4), ([(700, 300), (260, 9)], 2)])
+def test_attention_of_large_scores(cuda_lib, dtype, scale, lens, G):
+    """Scores of some hundreds, across rescalings and the join of parts.
+
+    A score is a sum of D products in 32 bits, off by at most D 2^-24 sum |q k|
+    |scale| =: e, and two roundings of its own size (scaling, and m c) add 2^-23 |score|
+    <= 2^-23 sum |q k| |scale|, below e.  A weight exp(s - m) is then off by at
+    most 4 e relatively (both scores, twice e each) and so is the sum of weights; over
+    both the output by 8 e mag, beside its roundings as at any scale.  lse: 2 e."""
+    D, Hk, page = 64, 2, 16
+    g = torch.Generator(device=DEV).manual_seed(1)
+    need = [-(-n // page) for n, _ in lens]
+    ids = np.random.default_rng(1).permutation(sum(need))
+    table, at = np.zeros((len(lens), max(need)), int), 0
+    for r, n in enumerate(need):
+        table[r, :n] = ids[at:at + n]
+        at += n
+    kc, vc = (torch.randn(sum(need), page, Hk, D, device=DEV, generator=g).to(dtype) for _ in range(2))
+    N = sum(l for _, l in lens)
+    q = (2 * torch.randn(N, Hk * G, D, device=DEV, generator=g)).to(dtype)
+    offs = np.concatenate([[0], np.cumsum([l for _, l in lens])])
+    err = dev_error()
+    out, lse = cuda_lib.spec_verify_attention(
+        q, kc, vc, i32(table), i32([n for n, _ in lens]), i32(offs), max_len=max(l for _, l in lens),
+        scale=scale, want_lse=True, dev_error=err)
+    assert err.item() == 0
+    o, x, qn = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().cpu().numpy()
+    for r, (n, l) in enumerate(lens):
+        k, v = (c[torch.tensor(table[r, :need[r]], device=DEV)].flatten(0, 1)[:n].double().cpu().numpy()
+                for c in (kc, vc))
+        rows = slice(offs[r], offs[r + 1])
+        want, wl, mag = S.attention_request(qn[rows], k, v, scale)
+        e = np.zeros((l, Hk * G))
+        for h in range(Hk * G):
+            e[:, h] = D * 2.0 ** -24 * abs(scale) * (np.abs(qn[rows][:, h]) @ np.abs(k[:, h // G]).T).max(1)
+        assert e.max() < 0.01
+        tol = mag * ((2.0 ** -12 if dtype == F32 else 2.0 ** -7) + 8 * e[:, :, None]) + 1e-30
+        assert (np.abs(o[rows] - want) <= tol).all(), np.max(np.abs(o[rows] - want) / tol)
+        assert (np.abs(x[rows] - wl) <= 2.0 ** -12 + 2 * e).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_at_the_ends_of_the_scales(cuda_lib, dtype):
+    """Scale 0 weighs all keys alike however large the products; the largest finite
+    scales pick the best key."""
+    n, D = 300, 64
+    g = torch.Generator(device=DEV).manual_seed(2)
+    q = torch.zeros(2, 1, D, device=DEV, dtype=dtype)
+    q[:, 0, 0] = 1e18
+    kc = torch.zeros(20, 16, 1, D, device=DEV, dtype=dtype)
+    kc[..., 0] = (torch.rand(20, 16, 1, device=DEV, generator=g) * 1e20).to(dtype)
+    vc = torch.randn(20, 16, 1, D, device=DEV, generator=g).to(dtype)
+    a = (i32(np.arange(20)[None]), i32([n]), i32([0, 2]))
+    out, lse = cuda_lib.spec_verify_attention(q, kc, vc, *a, max_len=2, scale=0.0, want_lse=True)
+    v = vc.flatten(0, 1)[:, 0].double()
+    for j in range(2):
+        want, mag = v[:n - 1 + j].mean(0), v[:n - 1 + j].abs().mean(0)
+        assert ((out[j, 0].double() - want).abs() <= 2.0 ** (-12 if dtype == F32 else -7) * mag).all()
+        assert abs(lse[j, 0].item() - np.log(n - 1 + j)) <= 2.0 ** -12
+    # a scale times log2(e) that leaves fp32: products of 0 and of 1
+    for scale in (3e38, -3e38):
+        q[:, 0, 0] = 1.0 if scale > 0 else -1.0
+        kc.zero_()
+        kc[7, 5, 0, 0] = 1.0
+        out, _ = cuda_lib.spec_verify_attention(q, kc, vc, *a, max_len=2, scale=scale)
+        assert torch.equal(out[:, 0], vc[7, 5].repeat(2, 1))
