@@ -279,7 +279,10 @@ int spec_verify_attention(const void* query, int64_t q_row_stride, int64_t q_hea
                    static_cast<const char*>(key_cache), static_cast<const char*>(value_cache),
                    block_stride * es, token_stride * es, head_stride * es, block_table,
                    table_stride, table_width, seq_lens, row_offsets, B, n_rows, max_len, heads,
-                   heads / kv_heads, head_dim, num_blocks, page_size, window,
+                   heads / kv_heads, head_dim, num_blocks, page_size,
+                   // no window where it holds every key; a row before the first key would
+                   // take position - window below 32 bits
+                   window >= static_cast<int64_t>(table_width) * page_size ? 0 : window,
                    // scale 0: masked scores stay -inf, and no finite product weighs: 2^128 2^-149
                    // is nothing beside 1
                    c == 0.0f ? 0x1p-149f : c,

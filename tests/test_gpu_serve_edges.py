@@ -198,3 +198,15 @@ def test_attention_at_the_ends_of_the_scales(cuda_lib, dtype):
         kc[7, 5, 0, 0] = 1.0
         out, _ = cuda_lib.spec_verify_attention(q, kc, vc, *a, max_len=2, scale=scale)
         assert torch.equal(out[:, 0], vc[7, 5].repeat(2, 1))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30, 10 ** 6])
+def test_attention_windows_past_every_context(cuda_lib, dtype, window):
+    """A window that holds every key is no window, for requests with more rows than
+    tokens too."""
+    lens = [(2, 9), (0, 3), (130, 140), (9001, 4), (17, 16)]
+    for G in (1, 4):
+        a = check_attention(cuda_lib, dtype, lens, 2, G, 64, 16, window=window)
+        b = check_attention(cuda_lib, dtype, lens, 2, G, 64, 16)
+        assert torch.equal(a, b)
