@@ -369,9 +369,10 @@ __global__ __launch_bounds__(attn_threads(NS), attn_per_sm(NS, DP)) void attn_mm
   auto full = [&](int u) { return smem_addr(&bars->full[u]); };
   auto empty = [&](int u) { return smem_addr(&bars->empty[u]); };
 
+  int before = 0;     // copying warps: units of the segments so far
+  uint32_t done = 0;  // product warps: the stream's P tiles so far
   if (warp >= kLoadWarp && warp < kMmaWarp) {
     // ---------------------------------------------------------- copies
-    int before = 0;  // units of the segments so far
     uint32_t err = 0;
     Segment g;
     if constexpr (TMA) {
@@ -438,13 +439,6 @@ __global__ __launch_bounds__(attn_threads(NS), attn_per_sm(NS, DP)) void attn_mm
           }
         }
         before += 2 * n;
-      }
-      if (timed_out) {  // no copy outlives the CTA
-        for (int i = 0; i < L::kUnits && i < before; ++i) {
-          const int at = before - 1 - i;
-          bool late = false;
-          mbar_wait(full(at % L::kUnits), (at / L::kUnits) & 1, late);
-        }
       }
     } else if (warp == kLoadWarp) {
       // rows copied one by one, 16 bytes a lane: lane's addresses are those of rows
@@ -520,7 +514,7 @@ __global__ __launch_bounds__(attn_threads(NS), attn_per_sm(NS, DP)) void attn_mm
                    to = __shfl_sync(~0u, tmem, 0) + kO + s * DP;
     int u = 0;
     uint32_t turn = 0;                     // parity of the ring's turn
-    uint32_t tiles = 0, done = 0;          // the stream's S and P tiles so far
+    uint32_t tiles = 0;                    // the stream's S tiles so far
     uint32_t qturn = 0;
     auto step = [&]() {
       if (++u == L::kUnits) u = 0, turn ^= 1;
@@ -860,7 +854,20 @@ __global__ __launch_bounds__(attn_threads(NS), attn_per_sm(NS, DP)) void attn_mm
   }
   if (timed_out && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_TIMEOUT);
   tmem_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(timed_out)) {
+    // Some warp gave up, and what it waited for may still be on its way: no copy
+    // and no product outlives the CTA.  All are issued by now, so the last units
+    // and the last product are each in the phase that is waited for.
+    bool late = false;
+    if (TMA && warp == kLoadWarp)
+      for (int i = 0; i < L::kUnits && i < before; ++i) {
+        const int at = before - 1 - i;
+        mbar_wait(full(at % L::kUnits), (at / L::kUnits) & 1, late);
+      }
+    if (warp >= kMmaWarp && done > 0)
+      mbar_wait(smem_addr(&bars->o[warp - kMmaWarp][(done - 1) & 1]), (done - 1) >> 1 & 1, late);
+    __syncthreads();
+  }
   tmem_fence_after();
   if (warp == kMmaWarp) tmem_free(tmem, kCols);
 }
