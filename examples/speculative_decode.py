@@ -41,14 +41,15 @@ class Toy:
         shape = (pages, page, kv_heads, head_dim)
         self.k, self.v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
 
-    def logits(self, tokens, plan, table, max_len):
-        """Logits of the new tokens [n], whose keys and values enter the cache."""
+    def logits(self, tokens, plan, table, max_len, error):
+        """Logits of the new tokens [n], whose keys and values enter the cache; the
+        operators' flags go to ``error``."""
         x = self.embed[tokens] + self.place[plan.positions.long()]
         qkv = (x @ self.qkv).view(len(tokens), -1, self.dim)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
-        sv.spec_verify_append(k, v, plan.slots, self.k, self.v)
+        sv.spec_verify_append(k, v, plan.slots, self.k, self.v, dev_error=error)
         a, _ = sv.spec_verify_attention(q, self.k, self.v, table, plan.seq_lens, plan.row_offsets,
-                                        max_len=max_len)
+                                        max_len=max_len, dev_error=error)
         h = 0.2 * x + 2 * (a.flatten(1) @ self.out)
         return torch.nn.functional.layer_norm(h.float(), h.shape[1:]).to(x.dtype) @ self.embed.T
 
@@ -96,7 +97,7 @@ def generate(target, draft, prompts, new_tokens, block, page, pages, width, temp
         plan = s.plan(s.context, lens, rows)
         flat = torch.tensor([t for p in prompts for t in p[:-1]], device=dev)
         for model in {id(m): m for m in (target, draft)}.values():
-            model.logits(flat, plan, s.table, int(lens.max()))
+            model.logits(flat, plan, s.table, int(lens.max()), s.error)
         s.context = s.context + lens
     last = torch.tensor([p[-1] for p in prompts], device=dev)
     out = [[] for _ in prompts]
@@ -110,7 +111,7 @@ def generate(target, draft, prompts, new_tokens, block, page, pages, width, temp
         tokens, rows_of = [last], []
         for j in range(block if block > 1 else 0):
             plan = s.plan(s.context + j, one, B)
-            x = draft.logits(tokens[-1], plan, s.table, 1)
+            x = draft.logits(tokens[-1], plan, s.table, 1, s.error)
             if j == block - 1:
                 break
             u = torch.rand(B, device=dev, generator=g).clamp_(max=1 - 2.0 ** -24)
@@ -119,7 +120,7 @@ def generate(target, draft, prompts, new_tokens, block, page, pages, width, temp
             rows_of.append(x)
         # the target over the whole block, and the verdict
         plan = s.plan(s.context, full, B * block)
-        x = target.logits(torch.stack(tokens, 1).flatten(), plan, s.table, block)
+        x = target.logits(torch.stack(tokens, 1).flatten(), plan, s.table, block, s.error)
         drafts = torch.stack(rows_of, 1).flatten(0, 1) if rows_of else x[:0]
         u = torch.rand(B * block, device=dev, generator=g).clamp_(max=1 - 2.0 ** -24)
         v = sv.spec_verify(x.contiguous(), drafts.contiguous(),

@@ -2,6 +2,9 @@
 requests that get no pages, calls without rows, scales and windows at the ends of
 their ranges, many rows of a real vocabulary."""
 
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -210,3 +213,24 @@ def test_attention_windows_past_every_context(cuda_lib, dtype, window):
         a = check_attention(cuda_lib, dtype, lens, 2, G, 64, 16, window=window)
         b = check_attention(cuda_lib, dtype, lens, 2, G, 64, 16)
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- example
+
+def test_the_example_sees_the_flags_of_every_operator(cuda_lib, monkeypatch):
+    """Lengths that attention refuses, slots that append refuses: decoding stops."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "speculative_decode.py")
+    spec = importlib.util.spec_from_file_location("speculative_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model = example.Toy(1009, 4, 2, 32, 50, 16, F32, 3)
+    plan = example.Server.plan
+    for break_it in (lambda p: p.seq_lens.fill_(10 ** 6), lambda p: p.slots.fill_(1 << 40)):
+        def broken(self, *a):
+            p = plan(self, *a)
+            break_it(p)
+            return p
+        monkeypatch.setattr(example.Server, "plan", broken)
+        with pytest.raises(AssertionError, match="device error"):
+            example.generate(model, model, [[5, 9], [7]], 4, 3, page=16, pages=50, width=8)
