@@ -1,9 +1,11 @@
-"""ctypes binding of libspecverify.so (the C ABI in include/spec_verify.h).
+"""Python binding of libspecverify.so: the C ABI in include/spec_verify.h and
+spec_verify_shard.h by ctypes, that in spec_verify_serve.h by a small host module.
 
-Argument marshalling only: every step of the verify path runs in the
-library's kernels.  torch is used for device memory (outputs, workspace)
-and for the current CUDA stream.  Importing this module fails loudly when
-the library has not been built -- there is no fallback path.
+Argument marshalling only: every step runs in the library's kernels.  torch is
+used for device memory (outputs, workspace) and for the current CUDA stream.
+Importing this module fails loudly when the library has not been built, and so
+does a serving operator's call when its host module is missing -- there is no
+fallback path.
 """
 
 from __future__ import annotations
@@ -12,6 +14,8 @@ import ctypes
 import os
 
 import torch
+
+from . import build as _build
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libspecverify.so")
@@ -23,7 +27,31 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _serve_calls  # noqa: E402  (linked to the library above)
+
+class _NoServeCalls:
+    """In place of the serving operators' host module: every call says why."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the serving operators' Python calls (_serve_calls.so) are not "
+                          f"available: {self._why}; the library's build step builds them")
+
+
+def _load_serve_calls():
+    # C++ over torch's headers: another torch's is not loaded, not even to look
+    built, here = _build.calls_built_for(), _build.calls_stamp()
+    if built not in (None, here):
+        return _NoServeCalls(f"built for {built}, this is {here}")
+    try:
+        from . import _serve_calls as calls  # linked to the library above
+        return calls
+    except ImportError as e:
+        return _NoServeCalls(e)
+
+
+_serve_calls = _load_serve_calls()
 
 SV_BF16, SV_FP32 = 0, 1
 SV_GREEDY, SV_SAMPLE = 0, 1

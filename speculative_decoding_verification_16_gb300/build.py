@@ -5,7 +5,9 @@
 One translation unit each for the verify step, its vocabulary-sharded form,
 slot maps and cache writes, sampling, and paged attention; one ``-gencode``,
 compiled in parallel, in-tree next to this file, with ``nvcc -shared``.
-Rebuilds only when a source or a header is newer than the library.
+Rebuilds only when a source or a header is newer than the library; the calls
+also where they were built for another torch or Python.  The verify step needs
+the library alone: where the calls cannot be built, that is a warning.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libspecverify.so")
 CALLS = os.path.join(HERE, "_serve_calls.so")
+CALLS_STAMP = CALLS + ".stamp"  # the torch and Python that the calls were built for
 CALLS_SOURCE = os.path.join(CSRC, "serve_calls.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "sv_shard.cu", "sv_slots.cu",
                                            "sv_sample.cu", "sv_attention.cu")]
@@ -54,10 +58,29 @@ def _run(tool, cmd, verbose):
         print(res.stdout + res.stderr)
 
 
+def calls_stamp() -> str:
+    """The torch and Python of this process, whose binary interfaces the calls need."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def calls_built_for():
+    """What the built calls need, None where that is not recorded."""
+    if not os.path.exists(CALLS_STAMP):
+        return None
+    with open(CALLS_STAMP) as f:
+        return f.read()
+
+
 def _build_calls(verbose: bool) -> None:
     import sysconfig
 
     import torch
+    for old in (CALLS, CALLS_STAMP):  # not left beside another library
+        if os.path.exists(old):
+            os.remove(old)
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     inc = [os.path.join(root, "include"),
@@ -70,6 +93,8 @@ def _build_calls(verbose: bool) -> None:
                  CALLS_SOURCE, "-o", CALLS + ".tmp", LIB, f"-L{lib}", "-ltorch_python", "-ltorch",
                  "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,$ORIGIN:{lib}"], verbose)
     os.replace(CALLS + ".tmp", CALLS)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(calls_stamp())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -80,8 +105,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
                       "-Xlinker", "-soname=libspecverify.so",
                       "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", LIB + ".tmp", "-lcudart"], verbose)
         os.replace(LIB + ".tmp", LIB)
-    if force or _stale(CALLS, [CALLS_SOURCE, LIB]):
-        _build_calls(verbose)
+    if force or _stale(CALLS, [CALLS_SOURCE, LIB]) or calls_built_for() != calls_stamp():
+        try:
+            _build_calls(verbose)
+        except (ImportError, OSError, RuntimeError) as e:
+            warnings.warn(f"the serving operators' Python calls were not built: {e}")
     return LIB
 
 

@@ -2,6 +2,10 @@
 entries refuse and accept without touching a device."""
 
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -52,3 +56,79 @@ def test_attention_without_rows_needs_no_rows_memory(lib):
                                    8, 8, 128, 9, 16, 0, ctypes.c_float(0.1), 0, None, 1024, 128,
                                    None, None, P, 1 << 40, None)
     assert ok == 0
+
+
+# ---------------------------------------------------------------- the host module
+
+PACKAGE = "speculative_decoding_verification_16_gb300"
+USE = f"""
+import torch
+from {PACKAGE} import binding
+assert binding.spec_verify_workspace_size(32, 512) > 0
+t = torch.zeros(1, 1, 8)
+try:
+    binding.spec_verify_append(t, t, torch.zeros(1, dtype=torch.int64), t[None], t[None])
+except ImportError as e:
+    print("ImportError:", e)
+except ValueError as e:
+    print("ValueError:", e)
+"""
+
+
+def use_copy(lib, tmp_path, calls, stamp):
+    """The package with the built library, and the host module or not."""
+    from speculative_decoding_verification_16_gb300 import build
+    to = tmp_path / PACKAGE
+    to.mkdir()
+    for f in os.listdir(build.HERE):
+        if f.endswith(".py"):
+            shutil.copy(os.path.join(build.HERE, f), to)
+    shutil.copy(build.LIB, to)
+    if calls:
+        shutil.copy(build.CALLS, to)
+    if stamp is not None:
+        (to / os.path.basename(build.CALLS_STAMP)).write_text(stamp)
+    r = subprocess.run([sys.executable, "-c", USE], cwd=tmp_path, capture_output=True, text=True,
+                       env={**os.environ, "PYTHONPATH": str(tmp_path)})
+    assert r.returncode == 0, r.stderr
+    return r.stdout
+
+
+def test_the_verify_step_needs_no_host_module(lib, tmp_path):
+    """The library alone is enough to import the binding; a serving operator says
+    what is missing."""
+    out = use_copy(lib, tmp_path, False, None)
+    assert out.startswith("ImportError") and "_serve_calls" in out
+
+
+def test_a_host_module_of_another_torch_is_not_loaded(lib, tmp_path):
+    out = use_copy(lib, tmp_path, True, "torch 1.0, cpython-30")
+    assert out.startswith("ImportError") and "torch 1.0" in out
+
+
+def test_the_host_module_is_loaded(lib, tmp_path):
+    from speculative_decoding_verification_16_gb300 import build
+    assert "CUDA device" in use_copy(lib, tmp_path, True, build.calls_stamp())
+
+
+def test_build_without_a_host_compiler_keeps_the_library(lib, tmp_path, monkeypatch):
+    from speculative_decoding_verification_16_gb300 import build
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_serve_calls.so"))
+    monkeypatch.setattr(build, "CALLS_STAMP", str(tmp_path / "_serve_calls.so.stamp"))
+
+    def no_compiler(tool, cmd, verbose):
+        raise FileNotFoundError(tool)
+    monkeypatch.setattr(build, "_run", no_compiler)
+    with pytest.warns(UserWarning, match="not built"):
+        assert build.build() == build.LIB
+
+
+def test_build_renews_the_host_module_for_another_torch(lib, tmp_path, monkeypatch):
+    from speculative_decoding_verification_16_gb300 import build
+    assert build.calls_built_for() == build.calls_stamp()
+    monkeypatch.setattr(build, "CALLS_STAMP", str(tmp_path / "stamp"))
+    (tmp_path / "stamp").write_text("torch 1.0, cpython-30")
+    built = []
+    monkeypatch.setattr(build, "_build_calls", built.append)
+    build.build()
+    assert built == [False]
