@@ -130,13 +130,14 @@ struct Launch {
   void* stream;
   Launch(PyObject* o, at::Device d) {
     if (!d.is_cuda()) throw BadValue("tensors must be on a CUDA device, got " + d.str());
+    stream = o == Py_None ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(d.index()).stream())
+                          : reinterpret_cast<void*>(integer(o, "stream"));
+    // last: what throws above leaves no device to put back
     const int now = c10::cuda::current_device();
     if (now != d.index()) {
       c10::cuda::set_device(d.index());
       before = now;
     }
-    stream = o == Py_None ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(d.index()).stream())
-                          : reinterpret_cast<void*>(integer(o, "stream"));
   }
   ~Launch() {
     if (before >= 0) c10::cuda::set_device(static_cast<c10::DeviceIndex>(before));
