@@ -61,7 +61,7 @@ constexpr float kInf = __builtin_huge_valf();
 struct SampleArgs {
   const char* logits;
   int64_t row_bytes;
-  int32_t V, C, slice, shift, stats;  // CTAs a row, vectors a slice, log2 vectors a group, most groups
+  int32_t V, C, slice, shift;  // CTAs a row, vectors a slice, log2 vectors a group
   const float* temperature;
   const int32_t* top_k;
   const float *top_p, *min_p, *uniforms;
@@ -85,7 +85,6 @@ struct Header {
   uint64_t sum[kWarps];
   int32_t count, pick, cut, group, groups;
   float kept, total, base;
-  int32_t verdict;  // 0: done, 1: search
 };
 constexpr int kHeaderBytes = (sizeof(Header) + 127) / 128 * 128;
 
@@ -1253,8 +1252,8 @@ extern "C" int spec_verify_sample(const void* logits, int64_t row_stride, int32_
   int shift = 3;
   while (shift < 5 && vecs > 4096 << shift) ++shift;
   while (shift > 0 && vecs < 512 << shift) --shift;
-  const int stats = (vecs >> shift) + 2;
-  const SampleArgs a{static_cast<const char*>(logits), row_stride * es, V, C, slice, shift, stats,
+  const int stats = (vecs >> shift) + 2;  // most groups
+  const SampleArgs a{static_cast<const char*>(logits), row_stride * es, V, C, slice, shift,
                      temperature, top_k, top_p, min_p, uniforms, out_tokens, out_probs, dev_error};
   const int smem = kHeaderBytes + stats * 8;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -42,6 +42,23 @@ def test_tokens_without_weight_are_never_drawn(cuda_lib, dtype, V):
         assert (prob > 0).all()
 
 
+@pytest.mark.parametrize("dtype,V,N", [(BF, 32003, 200), (F32, 20011, 330), (BF, 151936, 160)])
+def test_many_rows(cuda_lib, dtype, V, N):
+    """More rows than SMs, where a row has one CTA: settings of every kind, masked
+    rows among them."""
+    rng = np.random.default_rng(N)
+    x = rng.normal(0, 3, (N, V))
+    x[::5, :] += 12 * (rng.random((len(x[::5]), V)) < 20 / V)
+    x[3::20][rng.random((len(x[3::20]), V)) < 0.999] = -np.inf
+    x[3::20, V // 3] = 1.0
+    kind = np.arange(N) % 6
+    T = np.where(kind == 5, 0.0, rng.choice([0.6, 1.0, 1.3], N))
+    k = np.where((kind == 0) | (kind == 2), rng.choice([20, 1000, V], N), 0)
+    p = np.where((kind == 1) | (kind == 2), rng.uniform(0.7, 0.97, N), 1.0)
+    m = np.where(kind == 3, 0.05, 0.0)
+    check_sample(cuda_lib, torch.tensor(x, dtype=dtype, device=DEV), rng.random(N), T, k, p, m)
+
+
 # ---------------------------------------------------------------- shortage
 
 @pytest.mark.parametrize("dtype", [BF, F32])
