@@ -120,7 +120,8 @@ int spec_verify_slots(const int32_t* context_lens, const int32_t* verify_lens, i
  * position slots[i] % page_size of page slots[i] / page_size of the caches
  * ([num_blocks][page_size][kv_heads][head_dim], any strides of the first
  * three dimensions, the same for both caches).  A negative slot is skipped; one past the caches
- * raises SV_DEVERR_PAGE and is skipped.  Two rows with one slot: either.
+ * raises SV_DEVERR_PAGE and is skipped.  Where two rows have one slot, each of
+ * its 2 to 16 byte units, keys and values apart, may be that of either.
  */
 int spec_verify_append(const void* key, const void* value, int64_t k_row_stride,
                        int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
@@ -151,8 +152,10 @@ int spec_verify_append(const void* key, const void* value, int64_t k_row_stride,
  *               do not rise within [0, n_rows] raise it and the request's rows
  *               are not written.
  *  max_len      host upper bound of every l.
+ *  n_rows       0 is no error: nothing is done.
  *  head_dim     a multiple of 8, up to SV_ATTN_MAX_HEAD_DIM; heads a multiple
- *               of kv_heads.
+ *               of kv_heads.  table_width * page_size up to 2^30 - 1, n_rows *
+ *               heads up to 2^31 - 1 (SV_ERR_UNSUPPORTED).
  *  scale        factor of the scores, finite.
  *  window       <= 0: off.
  *  out          [n_rows][heads][head_dim] dtype, strides multiples of 16
@@ -160,6 +163,8 @@ int spec_verify_append(const void* key, const void* value, int64_t k_row_stride,
  *  out_lse      [n_rows][heads] float32 device or NULL.
  *  workspace    device scratch, 256-byte aligned, of at least
  *               spec_verify_attention_workspace_size bytes; needs no clearing.
+ *               The size is that of all SMs' partials, whatever the call's (bf16
+ *               heads of 128: 42 MB): a caller keeps one for all calls.
  *               Calls that share it must be ordered on the GPU.
  * bf16: scores and all sums are held in 32 bits, the weights exp(s - m) are
  * rounded to bf16 for the second product.  fp32: all in 32 bits.

@@ -479,7 +479,8 @@ def spec_verify_slots(context_lens, verify_lens, block_table, held, free_list, f
     pages of its context and new tokens; ``held`` [B] and ``free_count`` [1]
     are the counts before the call and are returned anew.  No result may share
     memory with them, ``context_lens`` or ``verify_lens``.  Returns SlotOutputs: prefix
-    sums of verify_lens [B + 1], sequence lengths [B], and for ``n_rows`` rows
+    sums of verify_lens [B + 1], sequence lengths [B] (-1: the request got no pages
+    or is out of range, and attention gives its rows zeros), and for ``n_rows`` rows
     (at least the sum of verify_lens; the length of ``slots`` if given) the
     positions int32 and slots int64."""
     if n_rows is None:
@@ -534,7 +535,8 @@ def spec_verify_attention(query, key_cache, value_cache, block_table, seq_lens, 
     seq_lens[r] tokens) over its pages of the caches, causal within the chunk;
     ``window`` > 0 keeps the last window keys of each row; ``scale`` defaults to
     head_dim ** -0.5; ``max_len`` is a host upper bound of the new tokens of a
-    request.  Returns (out, lse or None)."""
+    request.  ``workspace`` (alloc_attention_workspace) is best kept between calls.
+    Returns (out, lse or None)."""
     if out is None:
         out = _new(query.shape, query.dtype, query.device, stream)
     if lse is None and want_lse:

@@ -122,9 +122,10 @@ int join(const MmaArgs& p, int grid, int64_t items, int64_t joins, cudaStream_t 
   Device d;
   const int rc = device(&d);
   if (rc != SV_OK) return rc;
-  // few items in many parts (one request's verify step: 8 items in 21): four
-  // threads a column take a part of them each, 17.6 us a call against 23.8; many
-  // items in two parts: more and smaller blocks, 163 us against 175
+  // few items in many parts: four threads a column take a part of them each (one
+  // request's 16 tokens, 32/8 heads of 128, over 16,000 keys 27 us a call against 37; over
+  // 4,000, where an item has some 20 parts, 15.7 against 14.7); many items in two parts:
+  // more and smaller blocks (32 requests of mixed contexts 158 us against 170)
   if (grid >= 8 * items)
     return launch(attn_combine_kernel<MR, DP, 4, F32>,
                   dim3(static_cast<unsigned>(std::min<int64_t>(joins, 4 * d.sms))),

@@ -9,7 +9,7 @@
 // of K and Q beside 32 FMAs a warp and four dimensions.  32 requests of 16 tokens,
 // 32 heads over 8 of 128, 4,096 cached: 1.51 ms (22.9 TFLOP/s); with one warp a row
 // and no sharing of keys it was 11.7 ms.  8 single tokens, 8 heads of 64, 2,048
-// cached: 65 us, and 658 us without the split over keys.  A row alone in its item
+// cached: 69 us, and 658 us without the split over keys.  A row alone in its item
 // pays for its warp's other seven.
 #pragma once
 

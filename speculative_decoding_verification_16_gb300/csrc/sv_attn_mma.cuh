@@ -27,7 +27,12 @@
 // bytes bound it): two CTAs an SM, each with one stream; for heads above 128, whose
 // O fills half the tensor memory, one CTA an SM at any number of rows.
 // NS = 2 (longer chunks: the products bound it): one CTA an SM, two streams
-// over the same key/value tiles, the tensor core alternating between them.
+// over the same key/value tiles, the tensor core alternating between them.  At head_dim
+// 128 a stream's tile takes 8 x 48 + 4 x 64 = 640 cycles of the tensor core, Q K^T being
+// bound by reading both operands from shared memory, for 512 of arithmetic: no more
+// than 0.80 of the rate, of which 0.69 is reached.  One call has one NS, by max_len: single
+// tokens beside a chunk run with one of two streams idle (200 over 4,096 keys 500 us
+// alone, 722 with one chunk of 512 that alone takes 38).
 //
 // Keys and values come by tensor copies of whole page pieces (page sizes that
 // are a multiple of 64 or 8, 16, 32) and by 16-byte copies of single rows
@@ -200,8 +205,8 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
     total += sm->part[i];
   }
   // runs of at least three tiles: shorter ones cost more in partials and their join
-  // than they save (one request's verify step 17.8 us at one, 16.3 at three, 18.0 at
-  // four; 54 single tokens over up to 1,216 keys 24.8, 18.5, 19.1)
+  // than they save (one request's verify step 17.8 us at one, 15.7 at three, 18.2 at
+  // four; 8 requests of 16 tokens over up to 2,000 keys 22.1, 22.2, 21.2)
   const int workers = static_cast<int>(
       min(static_cast<int64_t>(gridDim.x), p.whole ? total : (total + kMinRun - 1) / kMinRun));
   const int me = blockIdx.x;

@@ -27,13 +27,16 @@
 // barrier all sum the C partials in rank order, so all decide alike.
 //
 // What bounds it.  One row: latency (151,936 bf16 under top-k 20 and top-p 0.95
-// 8.0 us: 1.3 us to the settings, 1.3 us for the row on eight SMs, 0.9 us of
+// 8.4 us: 1.3 us to the settings, 1.3 us for the row on eight SMs, 0.9 us of
 // cluster barriers, 3.5 us to decide).  Many rows: the stream at two CTAs an SM with
 // the decision's latency between, and 512 rows are 1.7 times what fits (512 rows of
 // 262,144 bf16, 268 MB: 65 us, 4.1 TB/s, 0.62 of the measured copy rate; four CTAs of
-// 256 threads an SM 61 us, but 32 rows with their own settings 66 us against 32).
+// 256 threads an SM 61 us, but 32 rows with their own settings took twice the time).
 // Rows whose cut needs the bins: instructions, four passes over the row (96 flat
-// fp32 rows of 129,280 under top-p 80 us).
+// fp32 rows of 129,280 under top-p 82 us), and at 64 registers a thread cut_by_bins and
+// search spill some 300 bytes each.  Masked rows under top-k with fewer unmasked
+// tokens than k: no bin holds the cut, and the search walks the keys down to -inf (10 of
+// 151,936 bf16 under top-k 20: 84 us, where an unmasked row takes 9).
 // Rows held in the cluster's shared memory instead of read again measured slower:
 // 180 us for the 512 rows where reading again took 86, the resident bytes waiting
 // through every decision.

@@ -67,7 +67,7 @@ int allow_smem(const void* kernel, int max_smem) {
 // entries below `held`, list entries below `free_count`.
 //
 // Latency bound: the launch, two dependent rounds of loads (lengths, then page
-// ids) and the block scan between them: 4.9 us for 32 requests of 16 tokens, 8.5 us
+// ids) and the block scan between them: 5.2 us for 32 requests of 16 tokens, 9.0 us
 // for 1,024 requests and 131,000 tokens, whose 1.6 MB take 0.24 us at the copy rate.
 constexpr int kSlotThreads = 512;
 constexpr int kSlotWarps = kSlotThreads / 32;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(const SlotsArgs a) 
 // A copy of rows to scattered places: U-byte units, one CTA a group of R rows,
 // a thread the same unit of each row of the group, so that its R loads are in
 // flight together.  HBM bound: every byte read and written once.  16,384 rows of
-// 8 x 128 bf16 (134 MB) 25.3 us, 5.3 TB/s, 0.79 of the measured copy rate; 512 rows
+// 8 x 128 bf16 (134 MB) 25.5 us, 5.3 TB/s, 0.79 of the measured copy rate; 512 rows
 // 2.8 us, of which the launch is most.
 constexpr int kAppendThreads = 256;
 
