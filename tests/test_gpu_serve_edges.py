@@ -42,6 +42,21 @@ def test_tokens_without_weight_are_never_drawn(cuda_lib, dtype, V):
         assert (prob > 0).all()
 
 
+@pytest.mark.parametrize("tail", [2.0 ** -23 * 1.7, 2.0 ** -23 * 1.3, 0.7, 0.3])
+def test_running_masses_do_not_drift(cuda_lib, tail):
+    """511 equal weights below the best: added one by one to a sum of 1 or more, each
+    rounds the same way, and the running mass at their end is off by 511 roundings
+    (2^-25 each, 1.5e-5 in all).  The draw has to stay within 1e-6 of the mass."""
+    V = 512
+    rng = np.random.default_rng(7)
+    x = np.full((40, V), np.log(tail))
+    x[np.arange(40), rng.integers(0, V, 40)] = 0.0
+    rest = 511 * tail / (1 + 511 * tail)
+    u = 1 - min(rest, 0.999) * (np.arange(40) + 0.5) / 40
+    check_sample(cuda_lib, torch.tensor(x, dtype=F32, device=DEV), u, k=[500] * 40)
+    check_sample(cuda_lib, torch.tensor(x, dtype=F32, device=DEV), u, p=[0.9999999] * 40)
+
+
 @pytest.mark.parametrize("dtype,V,N", [(BF, 32003, 200), (F32, 20011, 330), (BF, 151936, 160)])
 def test_many_rows(cuda_lib, dtype, V, N):
     """More rows than SMs, where a row has one CTA: settings of every kind, masked
