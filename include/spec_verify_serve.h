@@ -271,7 +271,9 @@ int spec_verify_rope_append(const void* query, int64_t q_row_stride, int64_t q_h
  *               sees the context's keys t > positions[row] - window (positions outside
  *               [seq - l, seq - 1] are brought there); of its own rows the mask decides.
  * Over codes, scores and sums are held in 32 bits and the weights are rounded to fp16:
- * 2^-11 of each, and of small ones 2^-32 of the row's largest.  Keys and values are exact
+ * 2^-11 of each, and of small ones 2^-32 of the row's largest, a weight counted with the
+ * largest power of two 2^e of its tile's values: a key's part of the output is off by at
+ * most 2^-32 448 w, w the row's largest softmax 2^e.  Keys and values are exact
  * but for rows far below the largest of their tile, the request's tokens 64 i .. 64 i + 63:
  * of rows whose exponent is more than 22 below the tile's largest (or below -102) up to
  * 2^-23 in units of 2^largest is lost.  Rows of the tile that a query does not see count

@@ -112,7 +112,7 @@ int attention_args(const AttnCall& c, AttnArgs* out) {
                   static_cast<char*>(c.out), c.o_row_stride * es, c.o_head_stride * es, c.out_lse,
                   c.dev_error, FastDiv::by(static_cast<uint32_t>(c.heads / c.kv_heads)),
                   FastDiv::by(static_cast<uint32_t>(c.page_size)),
-                  c.key_exps, c.value_exps, static_cast<int32_t>(c.e_block_stride),
+                  codes ? c.key_exps : nullptr, codes ? c.value_exps : nullptr, static_cast<int32_t>(c.e_block_stride),
                   static_cast<int32_t>(c.e_token_stride), static_cast<int32_t>(c.e_head_stride),
                   reinterpret_cast<const uint32_t*>(c.tree_mask), c.mask_words, c.positions};
   return SV_OK;

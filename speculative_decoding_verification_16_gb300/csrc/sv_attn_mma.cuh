@@ -85,7 +85,7 @@ struct MmaArgs {
   bool whole;             // items are not cut
   int32_t over;           // what an item costs beside its tiles, in tiles (below)
   AttnRecord* record;     // [kMaxWorkers]
-  float2* ml;             // [2 * kMaxWorkers][rows]: m c and l of the partials
+  float2* ml;             // [2 * kMaxWorkers][rows]: m c (of codes r) and l of the partials
   float4* o;              // [2 * kMaxWorkers][DP / 4][rows]
 };
 
@@ -364,16 +364,25 @@ __device__ __forceinline__ uint64_t tree_bits(const AttnArgs& a, const Segment& 
 // powers are taken relative to 2^E, 2^7 below its largest: the rows' factors
 // 2^(exp - E) are at most 2^7, exact down to 2^-15, 2^-22 of the largest; below, half of
 // fp16's smallest step may be lost, 2^-25 2^E, and rows of factors below 2^-24 are taken
-// for zeros.  The keys' E scales the tile's scores.  The values' E joins the exponent:
-// with the reference mo from the largest s c + E so far of the row, weights
-// 2^(s c + E - mo) are near 1 where they count, O is sum 2^(s c - mo) v as with bf16,
-// and l takes each tile's sum of weights times 2^-E.  Queries are brought into fp16's
-// range by a power of two a row, exactly but for elements 2^-38 of the row's largest.
-// Weights in fp16 have 11 bits, bf16's 8; mo lies kLift below the largest exponent, so
-// that the row's largest weight is at least 2^7 (and at most 2^15, O being rescaled
-// late) and what fp16 loses of a small one is at most 2^-25, 2^-32 of the largest.
+// for zeros.  Queries are brought into fp16's range by a power of two a row, 2^qe: its
+// largest element to [2^14, 2^15), so elements down to 2^-31 of the largest are exact and
+// smaller ones lose at most 2^-25, 2^-39 of it.  The keys' E and qe scale the tile's scores.
+//
+// Values of far apart E need references of their own for O and l: the key that counts
+// most in O, by s c + E, may count nothing in l, which knows no E, and the other way.  Of
+// a row r is the largest product q k so far (raised late, by 2^60), l is the sum of
+// 2^((q k - r) c), and O is held for the reference r c + D, D from the largest
+// s c + E - 7 = r c + D: a tile's weights are w = 2^(s c + E - r c - D), near 2^7 where they
+// count, O += w (v 2^-E) and l += 2^(D - E) w.  Where a tile's weights all lie below 2^-53,
+// their part of l is formed without E and D.  Weights in fp16 have 11 bits, bf16's 8; the
+// row's largest is at least 2^7 (kLift; and at most 2^15, O being rescaled late), and what
+// fp16 loses of a small one is at most 2^-25, 2^-32 of the largest.  A partial is O
+// 2^D / l, the part's own mean, with r and l.  (One reference for both, and l with 2^-E in
+// it: where E rose by 126 from one tile to the next, l lost the tiles before.)
 constexpr float kLift = 7.0f;
-constexpr int kFactorMin = -87;  // least E: 2^-E times the weights sums in fp32
+constexpr int kFactorMin = -87;  // least E: 2^D / l stays a normal number
+constexpr float kRaise = 60.0f;  // log2 of how far l's terms may exceed 1
+constexpr float kApart = 60.0f;
 // E of a tile whose rows' largest exponent is `most`.
 __device__ __forceinline__ int tile_exponent(int most) { return max(most - 7, kFactorMin); }
 
@@ -390,6 +399,8 @@ __device__ __forceinline__ uint32_t code_factor(int d) {  // 2^d twice, d <= 7
 __device__ __forceinline__ float pow2_any(int e) {  // 2^e, e in [-149, 127]
   return __uint_as_float(e >= -126 ? static_cast<uint32_t>(e + 127) << 23 : 0x400000u >> (-127 - e));
 }
+// x 2^e, e in [-252, 254]: two factors of one sign
+__device__ __forceinline__ float scaled(float x, int e) { return x * pow2(e >> 1) * pow2(e - (e >> 1)); }
 
 // ---------------------------------------------------------------- kernel
 template <int NS, int DP>
@@ -403,7 +414,8 @@ struct AttnSmem {
 struct AttnBars {
   uint64_t full[kMaxUnits], empty[kMaxUnits], raw[kMaxUnits];  // raw: codes are there
   uint64_t q[2], s[2][2], p[2][2], o[2][2], idle;  // by stream; s, p and o by S buffer too
-  int32_t key_exp[8], value_exp[8];  // of codes: E of a tile's keys and values
+  int32_t key_exp[8];  // of codes: E of a tile's keys
+  float value_exp[8];  // and values
   uint32_t tmem;
   int32_t odd;  // a non-finite value was set aside in this CTA
 };
@@ -534,7 +546,8 @@ __device__ __forceinline__ void turn_codes(const MmaArgs& p, Walk<NS * kRows> wa
         __syncwarp();
         // read when the tile's scores are formed.  The slot's last tile is done with: its
         // values' unit lies before the one just released
-        if (val == 0 && lane == 0) bars->key_exp[cur.tile & 7] = ek, bars->value_exp[cur.tile & 7] = ev;
+        if (val == 0 && lane == 0)
+          bars->key_exp[cur.tile & 7] = ek, bars->value_exp[cur.tile & 7] = static_cast<float>(ev);
         char* const unit = ring + u * L::kUnitBytes;
 #pragma unroll
         for (int part = 0; part < (DP == 256 ? 2 : 1); ++part) {
@@ -583,16 +596,16 @@ __device__ __forceinline__ void turn_codes(const MmaArgs& p, Walk<NS * kRows> wa
 }
 
 // The first `rows` rows of a warp's 32 of a query tile brought from bf16 into fp16's
-// range in place, a row's largest element to [2^14, 2^15).  Returns the power of two that
-// lane's row was divided by.  DP / 8 lanes a row, few instructions: run once an item,
-// they come from far away.
+// range in place, a row's largest element to [2^14, 2^15), and negated where the scale is
+// negative.  Returns log2 of what lane's row was divided by.  DP / 8 lanes a row, few
+// instructions: run once an item, they come from far away.
 template <int DP>
-__device__ __forceinline__ float query_to_fp16(char* tile, int lane, int rows) {
+__device__ __forceinline__ int query_to_fp16(char* tile, int lane, int rows, bool negated) {
   constexpr int kLanes = DP / 8, kEach = 32 / kLanes;  // of a row; rows at once
   constexpr int kFlight = 4;                           // such steps together
   const int j = lane % kLanes, sub = lane / kLanes;
   char* const at = tile + (j >> 3) * (kRows * 128);
-  float mine = 1.0f;
+  int mine = 0;
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += kFlight * kEach) {
     uint4 v[kFlight];
@@ -616,14 +629,14 @@ __device__ __forceinline__ float query_to_fp16(char* tile, int lane, int rows) {
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
       const int e = max(14, min(top[i], 254));  // 255: not finite, whatever the factor
-      const float f = pow2_any(141 - e);
+      const float f = negated ? -pow2_any(141 - e) : pow2_any(141 - e);
       uint32_t* w = reinterpret_cast<uint32_t*>(&v[i]);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(bf16hi(w[k]) * f), "f"(bf16lo(w[k]) * f));
       *unit(i) = v[i];
       const int other = __shfl_sync(~0u, e, lane % kEach * kLanes);  // of the step's row lane % kEach
-      if (lane / kEach == r0 / kEach + i) mine = pow2_any(other - 141);
+      if (lane / kEach == r0 / kEach + i) mine = other - 141;
     }
   }
   return mine;
@@ -928,8 +941,8 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
       __syncwarp();
       tmem_fence_after();
     };
-    float c = fabsf(a.scale2);
-    int cta_tiles = 0;   // of codes: tiles of the segments so far
+    const float c = fabsf(a.scale2);
+    int cta_tiles = 0, qe = 0;  // of codes: tiles of the segments so far; the row's power of two
     WarpWalk<MR>* const ww = walks + warp;
     uint32_t tiles = 0;  // the stream's tiles so far
     uint32_t idle = 0;   // parity of the next segment without rows here
@@ -982,8 +995,8 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
       if constexpr (CODES) {
         __syncwarp();  // the row came by the other lanes' copies
         if (work)
-          c = fabsf(a.scale2) * query_to_fp16<DP>(qbuf + st * L::kQBytes + wrow * 128, lane,
-                                                  min(32, g.rows - st * kRows - wrow));
+          qe = query_to_fp16<DP>(qbuf + st * L::kQBytes + wrow * 128, lane,
+                                 min(32, g.rows - st * kRows - wrow), a.scale2 < 0.0f);
       }
       fence_async_smem();
       mbar_arrive(smem_addr(&bars->q[st]));
@@ -994,8 +1007,8 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
       const int all_hi = g.seq - g.l + (TREE ? 0 : a.by_group.of(g.m * MR) + 1);
       const int all_lo = TREE ? tree_all_lo(a, g) : a.window > 0
           ? max(0, g.seq - g.l + a.by_group.of(g.m * MR + g.rows - 1) - a.window + 1) : 0;
-      // the largest score; of codes mo, the largest s c + E
-      float m = -kInf, l = 0.0f;
+      // the largest score; of codes r, and D
+      float m = -kInf, shift = 0.0f, l = 0.0f;
 
       if (!live) {
         mbar_wait(smem_addr(&bars->idle), idle, timed_out);
@@ -1066,10 +1079,6 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
           tmem_ld32(s_buf, reinterpret_cast<uint32_t*>(s));
           tmem_ld32(s_buf + 32, reinterpret_cast<uint32_t*>(s + 32));
           tmem_wait_ld();
-          if (a.scale2 < 0.0f) {
-#pragma unroll
-            for (int k = 0; k < kTile; ++k) s[k] = -s[k];
-          }
           if (edge) {
             const uint32_t low = static_cast<uint32_t>(bits), high = static_cast<uint32_t>(bits >> 32);
 #pragma unroll
@@ -1083,61 +1092,81 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
           for (int k = 4; k < kTile; k += 8)
 #pragma unroll
             for (int e = 0; e < 4 && k + 2 * e < kTile; ++e) mx[e] = fmaxf(fmaxf(mx[e], s[k + 2 * e]), s[k + 2 * e + 1]);
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // c with the keys' E, the values' E
-          const int slot = (cta_tiles + tile - g.tile0) & 7, e = bars->value_exp[slot];
-          const float ct = fminf(fmaxf(c * pow2_any(bars->key_exp[slot]), 0x1p-149f), FLT_MAX);
-          const float ev = static_cast<float>(e);
-          top = fmaf(top, ct, ev - kLift);
-          const bool first = tile == g.tile0, apart = !first && top < m - 60.0f;  // weights far below one
-          if (first) {
-            m = top;
+          const int slot = (cta_tiles + tile - g.tile0) & 7, unit = qe + bars->key_exp[slot];  // of the scores
+          const float top = scaled(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), unit);
+          const float ct = fminf(fmaxf(scaled(c, unit), 0x1p-149f), FLT_MAX);
+          const float e = bars->value_exp[slot];
+          bool apart = false;  // weights far below one
+          if (tile == g.tile0) {
+            m = top, shift = e - kLift;
           } else {
-            top = fmaxf(top, m);
-            const bool rise = top > -kInf && (m == -kInf || top - m > kRescale);
-            if (__any_sync(~0u, rise)) {
-              const float f = top > m ? ex2(m - top) : 1.0f;
-              wait_o(tiles - 1);
+            // log2 of the tile's largest above r, and of its weight above 2^7 (NaN, and no
+            // rise, where neither it nor the tiles before have a key)
+            const float above = (top - m) * c, most = above + (e - kLift) - shift;
+            const bool rise = most > kRescale, raise = rise || above > kRaise;
+            if (__any_sync(~0u, raise)) {
+              const float up = raise && top > m ? above : 0.0f;
+              const float now = rise ? (top > m ? 0.0f : above) + (e - kLift) : shift - up;
+              const float f = rise ? ex2(shift - up - now) : 1.0f;
+              l *= ex2(-up);
+              m = raise ? fmaxf(m, top) : m, shift = now;
+              if (__any_sync(~0u, rise)) {
+                wait_o(tiles - 1);
 #pragma unroll 1
-              for (int k = 0; k < DP; k += 16) {
-                uint32_t o[16];
-                tmem_ld16(o_at + k, o);
-                tmem_wait_ld();
+                for (int k = 0; k < DP; k += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(o_at + k, o);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st16(o_at + k, o);
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st16(o_at + k, o);
+                }
               }
-              l *= f;
-              m = top;
+            }
+            apart = most < -kApart && top > -kInf;
+          }
+          const float ref = m == -kInf ? 0.0f : m;
+          if (!__any_sync(~0u, apart)) {
+            const float base = fmaf(ref, c, shift - e);
+            const uint64_t mul2 = pack2(ct, ct), base2 = pack2(-base, -base);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < kTile; k += 32) {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float p0, p1;
+                unpack2(fma2(pack2(s[k + 2 * i], s[k + 2 * i + 1]), mul2, base2), &p0, &p1);
+                p0 = ex2(p0), p1 = ex2(p1);
+                sum[i & 1] = add2(sum[i & 1], pack2(p0, p1));
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(p1), "f"(p0));
+              }
+              tmem_st16(s_buf + k / 2, w);
+            }
+            float s0, s1;
+            unpack2(add2(sum[0], sum[1]), &s0, &s1);
+            l += (s0 + s1) * ex2(shift - e);
+          } else {
+            // weights so small that their part of l is a sum of its own.  S is read again, in a
+            // short loop: the other tiles' instructions barely fit the cache
+#pragma unroll 1
+            for (int k = 0; k < kTile; k += 4) {
+              uint32_t x[4], w[2];
+              tmem_ld4(s_buf + k, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float y = __uint_as_float(x[i]);
+                y = bits >> (k + i) & 1 ? fmaf(y, ct, -ref * c) : -kInf;
+                l += ex2(y);
+                x[i] = __float_as_uint(ex2(y - (shift - e)));
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(__uint_as_float(x[2 * i + 1])), "f"(__uint_as_float(x[2 * i])));
+              tmem_st2(s_buf + k / 2, w);
             }
           }
-          const float ref = m == -kInf ? 0.0f : m, base = m == -kInf ? 0.0f : m - ev;
-          const bool any_apart = __any_sync(~0u, apart);
-          const uint64_t mul2 = pack2(ct, ct), base2 = pack2(-base, -base);
-          uint64_t sum[2] = {0, 0};
-#pragma unroll
-          for (int k = 0; k < kTile; k += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float p0, p1;
-              unpack2(fma2(pack2(s[k + 2 * i], s[k + 2 * i + 1]), mul2, base2), &p0, &p1);
-              p0 = ex2(p0), p1 = ex2(p1);
-              sum[i & 1] = add2(sum[i & 1], pack2(p0, p1));
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(p1), "f"(p0));
-            }
-            tmem_st16(s_buf + k / 2, w);
-          }
-          float sum_apart = 0.0f;
-          if (any_apart) {
-            // values so small beside others' that their weights leave fp32: the weights'
-            // sum is formed without E
-#pragma unroll
-            for (int k = 0; k < kTile; ++k) sum_apart += ex2(fmaf(s[k], ct, -ref));
-          }
-          float s0, s1;
-          unpack2(add2(sum[0], sum[1]), &s0, &s1);
-          l += any_apart ? sum_apart : (s0 + s1) * pow2_any(-e);
           tmem_wait_st();
         }
         if (!CODES && work) {
@@ -1238,7 +1267,8 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
           const int head = g.h * a.group + i - a.by_group.of(i) * a.group;
           const int64_t orow = g.row0 + a.by_group.of(i);
           const int slot = 2 * blockIdx.x + (g.begins ? 1 : 0);
-          const float inv = g.whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+          float inv = g.whole || CODES ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+          if (CODES) inv *= ex2(shift);
           const int prow = st * kRows + row;
           // rolled where segments are short: unrolled, its instructions come from far away
 #pragma unroll (CODES ? 1 : DP / 64)
@@ -1289,13 +1319,14 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
 #pragma unroll
               for (int e = 0; e < 64; e += 4)
                 p.o[(static_cast<int64_t>(slot) * (DP / 4) + (k0 + e) / 4) * MR + prow] =
-                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    CODES ? make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv)
+                          : make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
           if (valid) {
-            const float mc = m == -kInf ? -kInf : CODES ? m : m * c;
+            const float mc = m == -kInf ? -kInf : m * c;
             if (!g.whole)
-              p.ml[static_cast<int64_t>(slot) * MR + prow] = make_float2(mc, l);
+              p.ml[static_cast<int64_t>(slot) * MR + prow] = make_float2(CODES ? m : mc, l);
             else if (a.lse != nullptr)
               a.lse[orow * a.heads + head] = l > 0.0f || l != l ? (mc + log2f(l)) * kLn2 : -kInf;
           }
@@ -1328,8 +1359,9 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
 //
 // Joins the partials of the items that were cut.  Every block finds all of them
 // from the workers' records and takes four rows at a time: the parts' weights
-// 2^(m c - max) go to shared memory, then GROUPS threads sum four columns of a row,
-// each over every GROUPS-th part, in worker order.  Bound by the latency of two rounds of loads,
+// 2^(m c - max) (of codes, whose parts are means, times l over the sum of those) go to
+// shared memory, then GROUPS threads sum four columns of a row, each over every GROUPS-th
+// part, in worker order.  Bound by the latency of two rounds of loads,
 // and by the partials' bytes (from L2) where there are many.
 constexpr int kCombineRows = 4;
 
@@ -1347,6 +1379,8 @@ __global__ __launch_bounds__(GROUPS * combine_group(DP)) void attn_combine_kerne
   __shared__ int32_t found[(kMaxWorkers + kCombineThreads - 1) / kCombineThreads * (kCombineThreads / 32)];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool codes = !F32 && a.k_exps != nullptr;
+  const float c = fabsf(a.scale2);
   grid_dep_wait();
   // the list is in worker order, the same in every block
   constexpr int kChunks = (kMaxWorkers + kCombineThreads - 1) / kCombineThreads;
@@ -1402,14 +1436,19 @@ __global__ __launch_bounds__(GROUPS * combine_group(DP)) void attn_combine_kerne
       if (top == -kInf) top = 0.0f;
       for (int i = lane; i < r.parts; i += 32) {
         const float2 x = p.ml[slot(i) * MR + row];
-        const float f = ex2(x.x - top);
-        weight[warp][i] = f;
+        const float f = ex2(codes ? (x.x - top) * c : x.x - top);
+        weight[warp][i] = codes ? x.y * f : f;
         l += x.y * f;
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+      if (codes) {  // before the sum: the parts may be as large as fp32 holds
+        top *= c;
+        for (int i = lane; i < r.parts; i += 32) weight[warp][i] *= inv;
+      }
       if (lane == 0) {
-        inverse[warp] = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        inverse[warp] = codes ? 1.0f : inv;
         const int j = r.m * MR + row;
         if (a.lse != nullptr)
           a.lse[(static_cast<int64_t>(r.row0) + a.by_group.of(j)) * a.heads + r.h * a.group + j -
