@@ -383,6 +383,7 @@ constexpr float kLift = 7.0f;
 constexpr int kFactorMin = -87;  // least E: 2^D / l stays a normal number
 constexpr float kRaise = 60.0f;  // log2 of how far l's terms may exceed 1
 constexpr float kApart = 60.0f;
+constexpr float kLargeScore = 1024.0f;  // of |r c|, from where on r c - D + E is off by 2^-14
 // E of a tile whose rows' largest exponent is `most`.
 __device__ __forceinline__ int tile_exponent(int most) { return max(most - 7, kFactorMin); }
 
@@ -1126,7 +1127,7 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
             apart = most < -kApart && top > -kInf;
           }
           const float ref = m == -kInf ? 0.0f : m;
-          if (!__any_sync(~0u, apart)) {
+          if (!__any_sync(~0u, apart || fabsf(ref * c) > kLargeScore)) {
             const float base = fmaf(ref, c, shift - e);
             const uint64_t mul2 = pack2(ct, ct), base2 = pack2(-base, -base);
             uint64_t sum[2] = {0, 0};
@@ -1147,8 +1148,12 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
             unpack2(add2(sum[0], sum[1]), &s0, &s1);
             l += (s0 + s1) * ex2(shift - e);
           } else {
+            // scores so large that the rounding of r c would neither cancel nor be the same
+            // beside each tile's E: differences of products first, exact where they count; or
             // weights so small that their part of l is a sum of its own.  S is read again, in a
-            // short loop: the other tiles' instructions barely fit the cache
+            // short loop: the other tiles' instructions barely fit the cache (unrolled: chunks
+            // 840 us for 760)
+            const float u0 = pow2(unit >> 1), u1 = pow2(unit - (unit >> 1));
 #pragma unroll 1
             for (int k = 0; k < kTile; k += 4) {
               uint32_t x[4], w[2];
@@ -1157,7 +1162,7 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float y = __uint_as_float(x[i]);
-                y = bits >> (k + i) & 1 ? fmaf(y, ct, -ref * c) : -kInf;
+                y = bits >> (k + i) & 1 ? (y * u0 * u1 - ref) * c : -kInf;
                 l += ex2(y);
                 x[i] = __float_as_uint(ex2(y - (shift - e)));
               }

@@ -124,3 +124,134 @@ def test_codes_of_tiles_far_apart(cuda_lib, steps, D, G, tree):
     check_numbers(cuda_lib, E4, lens, q, keys, vals, page, D ** -0.5, tree=tree)
     if not tree:
         check_numbers(cuda_lib, E4, lens, q, keys, vals, page, D ** -0.5, window=100)
+
+
+# Scores 2^17 + d of one unit each, exact in every type and in 32 bits: q k is 2^8 2^9 and
+# a product of small whole numbers d.  Their differences are exact too, so weights are as
+# far off as at any scale.  Over 16- and 32-bit caches scores are scaled before they are
+# subtracted while |score| log2 e is below 2^20: three roundings to 2^-24 of it.
+def counted(rng, lens, K, G, D, dtype):
+    N = sum(l for _, l in lens)
+    q = torch.zeros(N, K * G, D, device=DEV, dtype=dtype if dtype != E4 else BF)
+    q[..., 0] = 256.0
+    q[..., D - 1] = torch.tensor(rng.choice([1.0, 2.0, -1.0], (N, K * G)), device=DEV).to(q.dtype)
+    keys, vals = [], []
+    for n, _ in lens:
+        e = rng.integers(1, 5, (n, K))
+        k = np.zeros((n, K, D))
+        k[..., 0], k[..., D - 1] = 512.0, rng.integers(0, 8, (n, K))
+        v = some_codes(rng, n, K, D)
+        if dtype == E4:
+            tiles = rng.integers(-9, 9, (-(-n // 64), K))
+            keys.append((k / np.exp2(e)[..., None], e))
+            vals.append((v, tiles[np.arange(n) // 64] + rng.integers(-3, 1, (n, K))))
+        else:
+            keys.append((k, None))
+            vals.append((v, None))
+    return q, keys, vals
+
+
+LARGE = [[(300, 2), (40, 3), (3000, 5), (64, 64)], [(9001, 1), (700, 1)], [(700, 70), (90, 33)]]
+
+
+@pytest.mark.parametrize("scale", [0.5, -0.5, 40.0, 2.0 ** 11, -2.0 ** 13, 1e9, 1e30, -1e30])
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (256, 2)])
+def test_codes_of_large_scores(cuda_lib, scale, D, G):
+    """The best keys of scores up to 10^35 share a row's weight, across tiles whose powers
+    of two differ, rescalings and the join of parts."""
+    rng = np.random.default_rng(D)
+    for i, lens in enumerate(LARGE):
+        q, keys, vals = counted(rng, lens, 2, G, D, E4)
+        check_numbers(cuda_lib, E4, lens, q, keys, vals, 16, scale, tree=False, seed=i)
+        check_numbers(cuda_lib, E4, lens, q, keys, vals, 16, scale, tree=True, seed=i)
+
+
+@pytest.mark.parametrize("size", [2e4, 7e5, 3e7, 7e8, 3e10, 1e20])
+def test_codes_of_large_mixed_scores(cuda_lib, size):
+    """Random products at scales where a row's scores reach `size`.  A score is off by at
+    most D 2^-24 sum |q k| |scale|; where the best key leads by 64 of those and 64 more, the
+    output is its value."""
+    rng = np.random.default_rng(7)
+    n, l, K, G, D = 3001, 5, 2, 4, 64
+    scale = size / 40.0
+    q = torch.tensor(rng.standard_normal((l, K * G, D)), device=DEV).to(BF)
+    k, ke = some_codes(rng, n, K, D, most=4.0), np.zeros((n, K), int)
+    v, ve = some_codes(rng, n, K, D), np.repeat(rng.integers(-9, 9, (47, K)), 64, 0)[:n]
+    kc, e0, table = paged(np.random.default_rng(1), [(k, ke)], 16, K, D, E4)
+    vc, e1, _ = paged(np.random.default_rng(1), [(v, ve)], 16, K, D, E4)
+    out, lse = cuda_lib.spec_verify_attention(q, kc, vc, i32(table), i32([n]), i32([0, l]), max_len=l, scale=scale,
+                                              key_exps=e0, value_exps=e1, want_lse=True)
+    assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
+    clear, qn = 0, np64(q)
+    for j in range(l):
+        for h in range(K * G):
+            m = n - l + j + 1
+            s = scale * (k[:m, h // G] @ qn[j, h])
+            off = D * 2.0 ** -24 * scale * (np.abs(k[:m, h // G]) @ np.abs(qn[j, h])).max()
+            best = int(s.argmax())
+            s[best], top = -np.inf, s[best]
+            assert abs(lse[j, h].item() - top) <= 2 * off + 2.0 ** -22 * abs(top) + 9
+            if top - s.max() > 64 * off + 64:
+                clear += 1
+                want = v[best, h // G] * 2.0 ** float(ve[best, h // G])
+                assert (np.abs(np64(out[j, h]) - want) <= 2.0 ** -8 * np.abs(want)).all()
+    assert clear >= 20
+
+
+def test_codes_infinite_scores_and_the_ends_of_the_scales(cuda_lib):
+    """Scores far apart, the largest finite scales, whose scores leave fp32, and scale 0
+    under products of any size."""
+    n, D, page = 300, 64, 16
+    rng = np.random.default_rng(2)
+    v, ve = some_codes(rng, n, 1, D), rng.integers(-9, 9, (n, 1))
+    vc, e1, table = paged(np.random.default_rng(1), [(v, ve)], page, 1, D, E4)
+    a = (i32(table), i32([n]), i32([0, 2]))
+    q = torch.zeros(2, 1, D, device=DEV, dtype=BF)
+    value = v[:, 0] * np.exp2(ve.astype(np.float64))
+
+    def call(k, ke, scale):
+        kc, e0, _ = paged(np.random.default_rng(1), [(k, ke)], page, 1, D, E4)
+        out, lse = cuda_lib.spec_verify_attention(q, kc, vc, *a, max_len=2, scale=scale, key_exps=e0, value_exps=e1,
+                                                  want_lse=True)
+        return np64(out)[:, 0], np64(lse)[:, 0]
+    k, ke = np.zeros((n, 1, D)), np.zeros((n, 1), int)
+    # products up to 1e31
+    q[:, 0, 0] = 1.0
+    k[:, 0, 0], ke[:] = 8.0 + np.arange(n) % 8, np.minimum(np.arange(n) // 8, 30)[:, None] + 70
+    out, lse = call(k, ke, 1.0)
+    best = 247  # the largest product, first of those that repeat
+    top = k[:, 0, 0] * np.exp2(ke[:, 0].astype(np.float64))
+    for j in range(2):
+        ties = np.flatnonzero(top[:n - 1 + j] == top[best])
+        want, mag = value[ties].mean(0), np.abs(value[ties]).mean(0)
+        assert (np.abs(out[j] - want) <= 2.0 ** -7 * mag).all()
+        assert abs(lse[j] - top[best]) <= 2.0 ** -21 * top[best]
+    # scale 0: all keys alike
+    out, lse = call(k, ke, 0.0)
+    for j in range(2):
+        want, mag = value[:n - 1 + j].mean(0), np.abs(value[:n - 1 + j]).mean(0)
+        assert (np.abs(out[j] - want) <= 2.0 ** -7 * mag).all()
+        assert abs(lse[j] - math.log(n - 1 + j)) <= 2.0 ** -12
+    # scales whose product with log2 e leaves fp32: products of 0 and of 1, and of 0, 1 and 4
+    for scale in (3e38, -3e38):
+        q[:, 0, 0] = math.copysign(1.0, scale)
+        for more in (False, True):
+            k[:], ke[:] = 0, 0
+            k[120, 0, 0] = 1.0
+            best = 120
+            if more:
+                k[40, 0, 0], best = 4.0, 40
+            out, _ = call(k, ke, scale)
+            assert (out == np64(torch.tensor(value[best]).to(BF))).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [0.5, -0.5, 40.0, 2.0 ** 11, 1e9, -1e30])
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (256, 2)])
+def test_trees_of_large_scores(cuda_lib, dtype, scale, D, G):
+    rng = np.random.default_rng(D)
+    for i, lens in enumerate(LARGE):
+        q, keys, vals = counted(rng, lens, 2, G, D, dtype)
+        # three roundings of the score, twice in a weight and twice in the sum
+        e = 2.0 ** 17 * abs(scale) * 2.0 ** -24 * 3 if abs(scale) < 40 else 0.0
+        check_numbers(cuda_lib, dtype, lens, q, keys, vals, 16, scale, tree=True, seed=i, slack=4 * e, lse_slack=2 * e)
