@@ -15,7 +15,7 @@ namespace serve {
 
 namespace {
 
-template <int MR, int DP, bool F32>
+template <int MR, int DP, bool F32, bool CODES>
 int join_of(const MmaArgs& p, int grid, int64_t items, int64_t joins, cudaStream_t st) {
   if (grid == 1 || p.whole) return SV_OK;  // no item is cut
   Device d;
@@ -26,12 +26,22 @@ int join_of(const MmaArgs& p, int grid, int64_t items, int64_t joins, cudaStream
   // 4,000, where an item has some 20 parts, 15.7 against 14.7); many items in two parts:
   // more and smaller blocks (32 requests of mixed contexts 158 us against 170)
   if (grid >= 8 * items)
-    return launch(attn_combine_kernel<MR, DP, 4, F32>,
+    return launch(attn_combine_kernel<MR, DP, 4, F32, CODES>,
                   dim3(static_cast<unsigned>(std::min<int64_t>(joins, 4 * d.sms))),
                   4 * combine_group(DP), 0, 1, true, st, p, grid);
-  return launch(attn_combine_kernel<MR, DP, 1, F32>,
+  return launch(attn_combine_kernel<MR, DP, 1, F32, CODES>,
                 dim3(static_cast<unsigned>(std::min<int64_t>(joins, 16 * d.sms))), combine_group(DP),
                 0, 1, true, st, p, grid);
+}
+
+template <bool CODES>
+int join_mma(const MmaArgs& p, int mr, int dp, int grid, int64_t items, int64_t joins, cudaStream_t st) {
+  if (dp == 256) return join_of<kRows, 256, false, CODES>(p, grid, items, joins, st);
+  if (mr == kRows)
+    return dp == 64 ? join_of<kRows, 64, false, CODES>(p, grid, items, joins, st)
+                    : join_of<kRows, 128, false, CODES>(p, grid, items, joins, st);
+  return dp == 64 ? join_of<2 * kRows, 64, false, CODES>(p, grid, items, joins, st)
+                  : join_of<2 * kRows, 128, false, CODES>(p, grid, items, joins, st);
 }
 
 }  // namespace
@@ -39,15 +49,11 @@ int join_of(const MmaArgs& p, int grid, int64_t items, int64_t joins, cudaStream
 int join(const MmaArgs& p, int mr, int dp, bool f32, int grid, int64_t items, int64_t joins,
          cudaStream_t st) {
   if (f32)
-    return dp == 64    ? join_of<kFmaRows, 64, true>(p, grid, items, joins, st)
-           : dp == 128 ? join_of<kFmaRows, 128, true>(p, grid, items, joins, st)
-                       : join_of<kFmaRows, 256, true>(p, grid, items, joins, st);
-  if (dp == 256) return join_of<kRows, 256, false>(p, grid, items, joins, st);
-  if (mr == kRows)
-    return dp == 64 ? join_of<kRows, 64, false>(p, grid, items, joins, st)
-                    : join_of<kRows, 128, false>(p, grid, items, joins, st);
-  return dp == 64 ? join_of<2 * kRows, 64, false>(p, grid, items, joins, st)
-                  : join_of<2 * kRows, 128, false>(p, grid, items, joins, st);
+    return dp == 64    ? join_of<kFmaRows, 64, true, false>(p, grid, items, joins, st)
+           : dp == 128 ? join_of<kFmaRows, 128, true, false>(p, grid, items, joins, st)
+                       : join_of<kFmaRows, 256, true, false>(p, grid, items, joins, st);
+  return p.a.k_exps != nullptr ? join_mma<true>(p, mr, dp, grid, items, joins, st)
+                               : join_mma<false>(p, mr, dp, grid, items, joins, st);
 }
 
 // The checks of a call and the kernels' arguments.

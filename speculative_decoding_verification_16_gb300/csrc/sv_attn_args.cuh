@@ -47,17 +47,18 @@ struct AttnArgs {
 
 // Request r's rows and length.  Rows out of range: l = -1.  A length out of range (of
 // a tree: shorter than its rows too), or more rows than max_len: no key is seen, so
-// that the rows become zeros.  *bad is raised for both.
+// that the rows become zeros.  *bad is raised for both.  EXT: there may be masks.
 struct Span {
   int32_t row0, l, seq;
 };
+template <bool EXT>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int r, bool* bad = nullptr) {
   Span s;
   s.row0 = a.row_offsets[r];
   const int32_t end = a.row_offsets[r + 1];
   s.seq = a.seq_lens[r];
   const bool rows = s.row0 >= 0 && end >= s.row0 && end <= a.n_rows;
-  const bool keys = rows && end - s.row0 <= a.max_len && s.seq >= (a.mask != nullptr ? end - s.row0 : 0) &&
+  const bool keys = rows && end - s.row0 <= a.max_len && s.seq >= (EXT && a.mask != nullptr ? end - s.row0 : 0) &&
                     s.seq <= static_cast<int64_t>(a.table_width) * a.page;
   s.l = rows ? end - s.row0 : -1;
   if (!keys) s.seq = 0;

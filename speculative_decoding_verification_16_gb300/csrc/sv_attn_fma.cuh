@@ -38,10 +38,10 @@ __global__ __launch_bounds__(kFmaThreads) void attn_fma_kernel(const MmaArgs p) 
   float* const ps = vs + 2 * kFmaKeys * DP;           // [32 keys][kFmaWeights]
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Walk<MR> walk;
-  static_assert(sizeof(PlanSmem<MR>) <= 256, "plan block");
-  const bool any = plan<MR, kFmaThreads>(
-      p, reinterpret_cast<PlanSmem<MR>*>(ps + kFmaKeys * kFmaWeights), &walk);
+  Walk<MR, TREE> walk;
+  static_assert(sizeof(PlanSmem<MR, TREE>) <= 256, "plan block");
+  const bool any = plan<MR, kFmaThreads, TREE>(
+      p, reinterpret_cast<PlanSmem<MR, TREE>*>(ps + kFmaKeys * kFmaWeights), &walk);
   grid_dep_launch_dependents();
   if (!any) return;
   uint32_t err = 0;

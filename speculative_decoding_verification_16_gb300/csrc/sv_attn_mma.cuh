@@ -129,7 +129,11 @@ struct ItemTiles {
           // are not cut
 };
 
-template <int MR>
+// EXT, here and below: a call over codes or of trees, whose items cost `over` beside their
+// tiles and may have masks.  Other calls do without either: formed in their plan and walks
+// too, they took one block over 4,000 keys from 15.8 to 16.4 us, 32 x 16 tokens from 162 to
+// 165, chunks of 4,096 from 1,255 to 1,272.
+template <int MR, bool EXT>
 __device__ __forceinline__ ItemTiles item_tiles(const MmaArgs& p, const Span& s, int m) {
   const AttnArgs& a = p.a;
   ItemTiles t;
@@ -138,18 +142,18 @@ __device__ __forceinline__ ItemTiles item_tiles(const MmaArgs& p, const Span& s,
   const int j0 = a.by_group.of(m * MR), j1 = a.by_group.of(m * MR + t.rows - 1);
   t.kv_end = max(0, s.seq - s.l + j1 + 1);
   // a tree's rows may all lie at its root's position
-  const int kv_lo = a.window > 0 ? max(0, s.seq - s.l + (a.mask != nullptr ? 0 : j0) - a.window + 1) : 0;
+  const int kv_lo = a.window > 0 ? max(0, s.seq - s.l + (EXT && a.mask != nullptr ? 0 : j0) - a.window + 1) : 0;
   t.lo = kv_lo / kTile;
   t.tiles = max(1, (t.kv_end + kTile - 1) / kTile - t.lo);
-  t.n = p.whole ? 1 : t.tiles + p.over;
+  t.n = p.whole ? 1 : t.tiles + (EXT ? p.over : 0);
   return t;
 }
 
-template <int MR>
+template <int MR, bool EXT>
 __device__ __forceinline__ int64_t head_tiles(const MmaArgs& p, const Span& s) {
   int64_t n = 0;
   if (s.l > 0)
-    for (int m = 0; m * MR < s.l * p.a.group; ++m) n += item_tiles<MR>(p, s, m).n;
+    for (int m = 0; m * MR < s.l * p.a.group; ++m) n += item_tiles<MR, EXT>(p, s, m).n;
   return n;
 }
 
@@ -171,7 +175,7 @@ __device__ __forceinline__ int worker_of(int64_t total, int workers, int64_t u) 
 // (32 requests of 16 tokens over 512 to 32,768 in 8 bits: the last after 209 us, the mean
 // 145).  A run that ends within these units leaves the item to the next worker, which
 // starts it from its first tile.
-template <int MR>
+template <int MR, bool EXT>
 struct Walk {  // a worker's segments in order
   int r, h, m, off;
   int64_t left;
@@ -179,7 +183,7 @@ struct Walk {  // a worker's segments in order
 
   // What is left ends before the next item's tiles.
   __device__ __forceinline__ bool idle(const MmaArgs& p) const {
-    return off == 0 && !p.whole && left <= p.over;
+    return EXT && off == 0 && !p.whole && left <= p.over;
   }
   __device__ __forceinline__ bool next(const MmaArgs& p, Segment* g) {
     if (left <= 0) return false;
@@ -187,10 +191,11 @@ struct Walk {  // a worker's segments in order
       left = 0;
       return false;
     }
-    const ItemTiles t = item_tiles<MR>(p, s, m);
+    const ItemTiles t = item_tiles<MR, EXT>(p, s, m);
+    const int over = EXT ? p.over : 0;
     const int take = static_cast<int>(min(left, static_cast<int64_t>(t.n - off)));
     g->r = r, g->h = h, g->m = m, g->row0 = s.row0, g->l = s.l, g->seq = s.seq;
-    g->tile0 = t.lo + max(0, off - p.over), g->tile1 = t.lo + (p.whole ? t.tiles : off + take - p.over);
+    g->tile0 = t.lo + (EXT ? max(0, off - over) : off), g->tile1 = t.lo + (p.whole ? t.tiles : off + take - over);
     g->rows = t.rows, g->kv_end = t.kv_end;
     g->begins = off == 0, g->whole = off == 0 && take == t.n;
     left -= take;
@@ -201,7 +206,7 @@ struct Walk {  // a worker's segments in order
         m = 0;
         if (++h == p.kv_heads) {
           h = 0;
-          if (left > 0) do s = span_of(p.a, ++r); while (s.l <= 0);
+          if (left > 0) do s = span_of<EXT>(p.a, ++r); while (s.l <= 0);
         }
       }
     }
@@ -209,18 +214,18 @@ struct Walk {  // a worker's segments in order
   }
 };
 
-template <int MR>
+template <int MR, bool EXT>
 struct PlanSmem {
   int64_t part[16];
-  Walk<MR> walk;
+  Walk<MR, EXT> walk;
 };
 
 // Every CTA finds its own run from the requests' lengths: a scan over the
 // requests' tiles, then the thread whose request holds the run's start sets out
 // the walk.  More requests than threads: the tiles are formed twice, once for the
 // total and once up to the start.
-template <int MR, int THREADS>
-__device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR>* w) {
+template <int MR, int THREADS, bool EXT>
+__device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR, EXT>* sm, Walk<MR, EXT>* w) {
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kW = THREADS / 32;
@@ -228,8 +233,8 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
   int64_t mine = 0, per_head = 0;
   bool bad = false;
   for (int r = tid; r < a.B; r += THREADS) {
-    s = span_of(a, r, &bad);
-    per_head = head_tiles<MR>(p, s);
+    s = span_of<EXT>(a, r, &bad);
+    per_head = head_tiles<MR, EXT>(p, s);
     mine += per_head;
   }
   if (bad && blockIdx.x == 0 && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_LEN);
@@ -262,18 +267,18 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
   // by the thread with request r, `rem` tiles into it
   int item = -1;  // its item's tiles, in that thread
   auto set_out = [&](int r, int64_t rem) {
-    Walk<MR> x;
+    Walk<MR, EXT> x;
     x.r = r, x.s = s;
     x.h = rem < (1 << 30) && per_head < (1 << 30)
               ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(per_head))
               : static_cast<int>(rem / per_head);
     rem -= x.h * per_head;
     x.m = 0;
-    ItemTiles t = item_tiles<MR>(p, s, 0);
-    while (rem >= t.n) rem -= t.n, t = item_tiles<MR>(p, s, ++x.m);
+    ItemTiles t = item_tiles<MR, EXT>(p, s, 0);
+    while (rem >= t.n) rem -= t.n, t = item_tiles<MR, EXT>(p, s, ++x.m);
     x.off = static_cast<int>(rem);
     x.left = worker_start(total, workers, me + 1) - start;
-    if (!p.whole && x.off <= p.over) x.left += x.off, x.off = 0;  // from the first tile
+    if (EXT && !p.whole && x.off <= p.over) x.left += x.off, x.off = 0;  // from the first tile
     sm->walk = x;
     item = t.n;
   };
@@ -283,8 +288,8 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
     int64_t carry = 0;
     for (int base = 0; base < a.B && carry <= start; base += THREADS) {
       const int r = base + tid;
-      s = r < a.B ? span_of(a, r) : Span{0, 0, 0};
-      per_head = head_tiles<MR>(p, s);
+      s = r < a.B ? span_of<EXT>(a, r) : Span{0, 0, 0};
+      per_head = head_tiles<MR, EXT>(p, s);
       mine = per_head * p.kv_heads;
       inc = mine;
 #pragma unroll
@@ -310,10 +315,10 @@ __device__ __forceinline__ bool plan(const MmaArgs& p, PlanSmem<MR>* sm, Walk<MR
     AttnRecord rec{0, 0, 0, 0, 0};
     const int64_t first = start - w->off;  // the item's first tile
     int begins = worker_of(total, workers, first);  // the item's first worker
-    while (w->off > 0 && worker_start(total, workers, begins + 1) - first <= p.over) ++begins;
+    while (EXT && w->off > 0 && worker_start(total, workers, begins + 1) - first <= p.over) ++begins;
     if (w->off > 0 && begins == me - 1)
       rec = AttnRecord{worker_of(total, workers, first + item - 1) - me + 2,
-                       item_tiles<MR>(p, w->s, w->m).rows, w->s.row0, w->h, w->m};
+                       item_tiles<MR, EXT>(p, w->s, w->m).rows, w->s.row0, w->h, w->m};
     p.record[me] = rec;
   }
   return !w->idle(p);
@@ -447,9 +452,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-template <int MR>
+template <int MR, bool EXT>
 struct WarpWalk {
-  Walk<MR> walk;
+  Walk<MR, EXT> walk;
   Segment next;
 };
 
@@ -473,7 +478,7 @@ struct CodeTile {
 };
 
 template <int NS, int DP, int TURNERS, typename Raw, typename Full, typename Empty>
-__device__ __forceinline__ void turn_codes(const MmaArgs& p, Walk<NS * kRows> walk, int warp, int lane,
+__device__ __forceinline__ void turn_codes(const MmaArgs& p, Walk<NS * kRows, true> walk, int warp, int lane,
                                            char* ring, AttnBars* bars, Raw raw, Full full, Empty empty,
                                            bool& timed_out) {
   using L = AttnSmem<NS, DP>;
@@ -650,7 +655,8 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
   using L = AttnSmem<NS, DP>;
   constexpr int MR = NS * kRows;
   constexpr int kThreads = attn_threads(NS, DP, SRC), kTurners = attn_turners(NS, DP, SRC);
-  constexpr bool TMA = SRC == kTensorCopies || SRC == kCodeTensor, CODES = of_codes(SRC);
+  constexpr bool TMA = SRC == kTensorCopies || SRC == kCodeTensor, CODES = of_codes(SRC),
+                 EXT = CODES || TREE;
   // a unit as it is copied: chunks of columns side by side, each of 64 rows
   constexpr int kCopyChunks = !CODES ? L::kChunks : DP == 256 ? 2 : 1;
   constexpr int kCopyRow = CODES && DP == 64 ? 64 : 128;  // bytes of a row of a chunk
@@ -665,8 +671,8 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
   char* const qbuf = smem;
   char* const ring = smem + NS * L::kQBytes;
   AttnBars* const bars = reinterpret_cast<AttnBars*>(ring + L::kUnits * L::kUnitBytes);
-  WarpWalk<MR>* const walks = reinterpret_cast<WarpWalk<MR>*>(reinterpret_cast<char*>(bars) + kBarBytes);
-  static_assert(sizeof(WarpWalk<MR>) <= 104, "walk block");
+  WarpWalk<MR, EXT>* const walks = reinterpret_cast<WarpWalk<MR, EXT>*>(reinterpret_cast<char*>(bars) + kBarBytes);
+  static_assert(sizeof(WarpWalk<MR, EXT>) <= 104, "walk block");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kSoftmax = NS * 4, kLoadWarp = kSoftmax, kMmaWarp = kSoftmax + NS,
                 kTurnWarp = kMmaWarp + NS;
@@ -691,8 +697,8 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(smem_addr(&bars->tmem), kCols);
-  Walk<MR> walk;
-  const bool any = plan<MR, kThreads>(p, reinterpret_cast<PlanSmem<MR>*>(ring), &walk);
+  Walk<MR, EXT> walk;
+  const bool any = plan<MR, kThreads, EXT>(p, reinterpret_cast<PlanSmem<MR, EXT>*>(ring), &walk);
   grid_dep_launch_dependents();
   tmem_fence_before();
   __syncthreads();  // and the plan's scratch becomes the ring
@@ -944,7 +950,7 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
     };
     const float c = fabsf(a.scale2);
     int cta_tiles = 0, qe = 0;  // of codes: tiles of the segments so far; the row's power of two
-    WarpWalk<MR>* const ww = walks + warp;
+    WarpWalk<MR, EXT>* const ww = walks + warp;
     uint32_t tiles = 0;  // the stream's tiles so far
     uint32_t idle = 0;   // parity of the next segment without rows here
     int u0 = 0;          // ring position of the segment's first unit, and its turn
@@ -953,7 +959,7 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
     auto advance = [&]() {
       __syncwarp();
       if (lane == 0) {
-        Walk<MR> w = ww->walk;
+        Walk<MR, EXT> w = ww->walk;
         Segment n;
         if (!w.next(p, &n)) n.tile1 = -1;
         ww->walk = w;
@@ -1373,7 +1379,7 @@ constexpr int kCombineRows = 4;
 // threads of a group: four rows of DP / 4 columns, a whole number of warps per row
 __host__ __device__ constexpr int combine_group(int dp) { return dp < 128 ? 128 : dp; }
 
-template <int MR, int DP, int GROUPS, bool F32>
+template <int MR, int DP, int GROUPS, bool F32, bool CODES>
 __global__ __launch_bounds__(GROUPS * combine_group(DP)) void attn_combine_kernel(const MmaArgs p,
                                                                                   int workers) {
   constexpr int kGroup = combine_group(DP), kCombineThreads = GROUPS * kGroup, kCombineGroups = GROUPS;
@@ -1384,8 +1390,7 @@ __global__ __launch_bounds__(GROUPS * combine_group(DP)) void attn_combine_kerne
   __shared__ int32_t found[(kMaxWorkers + kCombineThreads - 1) / kCombineThreads * (kCombineThreads / 32)];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool codes = !F32 && a.k_exps != nullptr;
-  const float c = fabsf(a.scale2);
+  const float c = CODES ? fabsf(a.scale2) : 1.0f;
   grid_dep_wait();
   // the list is in worker order, the same in every block
   constexpr int kChunks = (kMaxWorkers + kCombineThreads - 1) / kCombineThreads;
@@ -1441,19 +1446,19 @@ __global__ __launch_bounds__(GROUPS * combine_group(DP)) void attn_combine_kerne
       if (top == -kInf) top = 0.0f;
       for (int i = lane; i < r.parts; i += 32) {
         const float2 x = p.ml[slot(i) * MR + row];
-        const float f = ex2(codes ? (x.x - top) * c : x.x - top);
-        weight[warp][i] = codes ? x.y * f : f;
+        const float f = ex2(CODES ? (x.x - top) * c : x.x - top);
+        weight[warp][i] = CODES ? x.y * f : f;
         l += x.y * f;
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
       const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-      if (codes) {  // before the sum: the parts may be as large as fp32 holds
+      if (CODES) {  // before the sum: the parts may be as large as fp32 holds
         top *= c;
         for (int i = lane; i < r.parts; i += 32) weight[warp][i] *= inv;
       }
       if (lane == 0) {
-        inverse[warp] = codes ? 1.0f : inv;
+        inverse[warp] = CODES ? 1.0f : inv;
         const int j = r.m * MR + row;
         if (a.lse != nullptr)
           a.lse[(static_cast<int64_t>(r.row0) + a.by_group.of(j)) * a.heads + r.h * a.group + j -
