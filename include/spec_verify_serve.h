@@ -340,7 +340,8 @@ int spec_verify_tree_accept(const int32_t* tokens, const int32_t* next_tokens,
 /*
  * Keys and values of the accepted paths, moved together: the cache row at slot
  * slots[row0 + path[row0 + j]] goes to slots[row0 + j] for 1 <= j <= accept_len[r], as
- * if all were read before any is written, in every layer.  A slot below 0 at either end
+ * if all were read before any is written, in every layer; row 0 stays, wherever the path
+ * starts.  A slot below 0 at either end
  * leaves that row out, one past the caches does and raises SV_DEVERR_PAGE.  A path that
  * does not rise, path[j] < j or path[j] >= l, ends there (SV_DEVERR_TREE); an accept_len
  * outside [-1, l - 1] raises SV_DEVERR_LEN and moves nothing of the request.

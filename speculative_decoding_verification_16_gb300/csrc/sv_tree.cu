@@ -201,8 +201,9 @@ __global__ __launch_bounds__(kMoveThreads) void tree_move_kernel(const MoveArgs 
   uint32_t err = 0;
   for (int j = tid; j <= n; j += kMoveThreads) {
     const int at = a.path[s.row0 + j], before = j > 0 ? a.path[s.row0 + j - 1] : -1;
-    // 0: stays; 1: moves; 2: the path ends here, it does not rise
-    ok[j] = at <= before || at < j || at >= s.l ? 2 : at == j ? 0 : 1;
+    // 0: stays, as row 0 does wherever the path starts; 1: moves; 2: the path ends here, it
+    // does not rise
+    ok[j] = at <= before || at < j || at >= s.l ? 2 : at == j || j == 0 ? 0 : 1;
     if (ok[j] == 1) {
       const int64_t f = a.slots[s.row0 + at], t = a.slots[s.row0 + j];
       from[j] = f, to[j] = t;

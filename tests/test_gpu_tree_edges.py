@@ -255,3 +255,31 @@ def test_trees_of_large_scores(cuda_lib, dtype, scale, D, G):
         # three roundings of the score, twice in a weight and twice in the sum
         e = 2.0 ** 17 * abs(scale) * 2.0 ** -24 * 3 if abs(scale) < 40 else 0.0
         check_numbers(cuda_lib, dtype, lens, q, keys, vals, 16, scale, tree=True, seed=i, slack=4 * e, lse_slack=2 * e)
+
+
+# ---------------------------------------------------------------- paths and moves
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_tree_move_leaves_row_0(cuda_lib, dtype):
+    """Rows 1 .. accept_len are moved to; a path that starts behind row 0 leaves the last
+    accepted token's keys and values as they are."""
+    L, page, K, D, l = 3, 4, 2, 32, 7
+    g = torch.Generator(device=DEV).manual_seed(1)
+    c = [torch.randint(0, 120, (L, 4, page, K, D), device=DEV, generator=g, dtype=torch.uint8).view(E4) if dtype == E4
+         else torch.randn(L, 4, page, K, D, device=DEV, generator=g).to(dtype) for _ in range(2)]
+    e = [torch.randint(-9, 9, (L, 4, page, K), device=DEV, generator=g, dtype=torch.int8) if dtype == E4 else None
+         for _ in range(2)]
+    slots = torch.tensor([9, 3, 12, 0, 7, 15, 5, 1, 2], device=DEV)
+    path, n, offs = [2, 4, 5, -1, -1, -1, -1, 1, -1], [2, 0], [0, l, 9]
+    raw = [x.view(torch.uint8) if dtype == E4 else x for x in c] + [x for x in e if x is not None]
+    want = [x.clone() for x in raw]
+    for x, w in zip(raw, want):
+        for j in (1, 2):
+            s, d = int(slots[path[j]]), int(slots[j])
+            w[:, d // page, d % page] = x[:, s // page, s % page]
+    err = dev_error()
+    cuda_lib.spec_verify_tree_move(i32(path), i32(n), i32(offs), slots, *c, max_len=8, key_exps=e[0], value_exps=e[1],
+                                   dev_error=err)
+    assert err.item() == 0
+    for x, w in zip(raw, want):
+        assert torch.equal(x, w)
