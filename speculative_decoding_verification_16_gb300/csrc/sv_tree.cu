@@ -193,7 +193,7 @@ __global__ __launch_bounds__(kMoveThreads) void tree_move_kernel(const MoveArgs 
   const int tid = threadIdx.x, r = blockIdx.x;
   const TreeSpan s = tree_span(a.row_offsets, r, a.n_rows);
   const int n = a.accept_len[r];  // moves of rows 1 .. n
-  if (s.l < 0 || s.l > a.max_len || n < -1 || n >= max(s.l, 1)) {
+  if (s.l < 0 || s.l > a.max_len || n < -1 || n >= s.l) {
     if (tid == 0 && blockIdx.y == 0 && a.dev_error != nullptr) atomicOr(a.dev_error, SV_DEVERR_LEN);
     return;
   }

@@ -283,3 +283,13 @@ def test_tree_move_leaves_row_0(cuda_lib, dtype):
     assert err.item() == 0
     for x, w in zip(raw, want):
         assert torch.equal(x, w)
+
+
+def test_tree_move_of_a_request_without_rows(cuda_lib):
+    """Without rows the length is -1; any other is out of range."""
+    c = torch.zeros(2, 4, 1, 8, device=DEV)
+    for n, flag in ((-1, 0), (0, cuda_lib.SV_DEVERR_LEN), (1, cuda_lib.SV_DEVERR_LEN)):
+        err = dev_error()
+        cuda_lib.spec_verify_tree_move(i32([0, -1]), i32([n, 0]), i32([0, 0, 2]), torch.arange(2, device=DEV), c,
+                                       c.clone(), max_len=4, dev_error=err)
+        assert err.item() == flag, n
