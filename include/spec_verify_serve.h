@@ -315,8 +315,10 @@ int spec_verify_tree(const int32_t* parents, const int32_t* seq_lens, const int3
 /*
  * The accepted path of every request's tree.  It starts at row 0; from a row it goes
  * on to that child whose token is the row's next token (of several the lowest), as long
- * as there is one.  With next_tokens sampled from the target's rows (spec_verify_sample)
- * the tokens given out are distributed as the target's, whatever was drafted.
+ * as there is one; none follows a next token below 0, which spec_verify_sample gives
+ * where it can draw none.  With next_tokens sampled from the target's rows
+ * (spec_verify_sample) the tokens given out are distributed as the target's, whatever was
+ * drafted.
  *
  *  tokens, next_tokens, parents  [n_rows] int32 device: each row's own token, the
  *                  target's after it, and the parents as above (ones out of range raise

@@ -67,10 +67,10 @@ def ancestors(parents):
 
 
 def accept(tokens, nxt, parents):
-    """(path, tokens given out) of one request."""
+    """(path, tokens given out) of one request; a next token below 0 is none."""
     at, path = 0, [0]
     while True:
-        kids = [c for c in range(at + 1, len(tokens)) if parents[c] == at and tokens[c] == nxt[at]]
+        kids = [c for c in range(at + 1, len(tokens)) if parents[c] == at and tokens[c] == nxt[at] >= 0]
         if not kids:
             return path, [nxt[i] for i in path]
         at = kids[0]

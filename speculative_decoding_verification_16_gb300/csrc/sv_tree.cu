@@ -103,8 +103,9 @@ __global__ __launch_bounds__(kTreeRows) void tree_plan_kernel(const PlanArgs a) 
 // ---------------------------------------------------------------- the accepted path
 //
 // A CTA a request, a thread a row: each row whose token is the one that the target
-// gave after its parent offers itself to it, the lowest wins; one thread walks down
-// from the root.  Bound by latency: three rounds of loads and the walk.
+// gave after its parent offers itself to it, the lowest wins (none where that is -1, no
+// token: a draft that could not be sampled is -1 too); one thread walks down from the root.
+// Bound by latency: three rounds of loads and the walk.
 struct AcceptArgs {
   const int32_t *tokens, *next, *parents, *row_offsets;
   int32_t B, n_rows, max_len;
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(kTreeRows) void tree_accept_kernel(const AcceptArgs
     }
   }
   __syncthreads();
-  if (p >= 0 && token == after[p]) atomicMin(&child[p], i);
+  if (p >= 0 && token >= 0 && token == after[p]) atomicMin(&child[p], i);
   __syncthreads();
   if (i == 0) {
     int at = 0, n = 0;

@@ -293,3 +293,13 @@ def test_tree_move_of_a_request_without_rows(cuda_lib):
         cuda_lib.spec_verify_tree_move(i32([0, -1]), i32([n, 0]), i32([0, 0, 2]), torch.arange(2, device=DEV), c,
                                        c.clone(), max_len=4, dev_error=err)
         assert err.item() == flag, n
+
+
+def test_tree_accept_stops_where_no_token_was_sampled(cuda_lib):
+    """A row whose token could not be sampled (-1) is followed by no row, one of a drafter
+    that failed too among them."""
+    tokens, nxt = [5, -1, 3, 4, 5, 6], [-1, 3, 4, 7, 6, -1]
+    parents, offs = [-1, 0, 1, 2, -1, 0], [0, 4, 6]
+    out, path, n = cuda_lib.spec_verify_tree_accept(i32(tokens), i32(nxt), i32(parents), i32(offs), max_len=4)
+    assert n.tolist() == [0, 1]
+    assert path.tolist() == [0, -1, -1, -1, 0, 1] and out.tolist() == [-1] * 4 + [6, -1]
