@@ -349,7 +349,11 @@ Rotation rotation(PyObject* positions, PyObject* freqs, PyObject* interleaved, P
     if (positions == Py_None) throw BadValue("positions are needed where freqs are given");
     r.positions = static_cast<int32_t*>(flat(positions, "positions", at::kInt, {rows}, d));
   }
-  r.interleaved = PyObject_IsTrue(interleaved) == 1 ? 1 : 0;
+  r.interleaved = PyObject_IsTrue(interleaved);
+  if (r.interleaved < 0) {
+    PyErr_Clear();
+    throw BadType("interleaved must be true or false");
+  }
   r.amplitude = static_cast<float>(number(amplitude, "amplitude"));
   return r;
 }
