@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from oracle import tree_oracle as T
-from test_gpu_tree import BF, DEV, E4, F32, dev_error, i32, np64, pack, random_tree
+from test_gpu_tree import (BF, DEV, E4, F32, check_attention, check_rope_append, close, dev_error, heads_of, i32,
+                           make_caches, np64, pack, random_tree, some_freqs, tree_state, values)
 
 pytestmark = pytest.mark.gpu
 
@@ -303,3 +304,145 @@ def test_tree_accept_stops_where_no_token_was_sampled(cuda_lib):
     out, path, n = cuda_lib.spec_verify_tree_accept(i32(tokens), i32(nxt), i32(parents), i32(offs), max_len=4)
     assert n.tolist() == [0, 1]
     assert path.tolist() == [0, -1, -1, -1, 0, 1] and out.tolist() == [-1] * 4 + [6, -1]
+
+
+# ---------------------------------------------------------------- rotary positions of many rows
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("D,R", [(64, 64), (128, 128), (256, 64), (80, 40), (128, 24), (96, 0)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_append_of_many_rows(cuda_lib, dtype, quant, D, R, interleaved):
+    """Rows enough for a warp each, and heads enough for several rounds of a warp's loads."""
+    check_rope_append(cuda_lib, dtype, quant, 1300, 21, 9, D, R, 16, "heads" if interleaved else "tokens", False, D + R,
+                      interleaved=interleaved)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("n,H,K,page,strided", [(1300, 0, 3, 7, True), (1501, 5, 1, 1, True), (1216, 17, 5, 64, False)])
+def test_rope_append_of_many_rows_of_any_layout(cuda_lib, quant, n, H, K, page, strided):
+    for dtype, D, R, layout in ((BF, 128, 64, "heads"), (F32, 64, 64, "tokens"), (BF, 72, 24, "tokens")):
+        check_rope_append(cuda_lib, dtype, quant, n, H, K, D, R, page, layout, strided, n + D)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,R", [(128, 128), (64, 24), (256, 256)])
+def test_rope_of_many_rows_and_heads(cuda_lib, dtype, D, R):
+    rng = np.random.default_rng(D)
+    g = torch.Generator(device=DEV).manual_seed(D)
+    for interleaved in (False, True):
+        x = heads_of(g, 2500, 37, D, dtype, interleaved)
+        f, pos = some_freqs(rng, R // 2), rng.integers(0, 100000, 2500)
+        kw = dict(interleaved=interleaved, amplitude=1.25)
+        freqs = torch.tensor(f.view(np.int64), device=DEV)
+        out = cuda_lib.spec_verify_rope(x, i32(pos), freqs, **kw)
+        close(out, *T.rope(np64(x), pos, f, interleaved, 1.25), dtype)
+        cuda_lib.spec_verify_rope(x, i32(pos), freqs, out=x, **kw)  # in place
+        assert torch.equal(x, out)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_rope_append_of_many_rows_skips_slots(cuda_lib, quant):
+    """Slots below 0 and past the cache leave it as it is, among rows of all others."""
+    n, K, D, page, blocks = 4000, 2, 64, 16, 200
+    rng = np.random.default_rng(3)
+    k = torch.randn(n, K, D, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3)).to(BF)
+    slots = np.full(n, -1)
+    slots[1::2] = blocks * page + rng.integers(0, 2 ** 40, n // 2)
+    on = rng.permutation(n)[:1500]
+    slots[on] = rng.permutation(blocks * page)[:1500]
+    kc = torch.full((blocks, page, K, D), 3.0, device=DEV).to(E4 if quant else BF)
+    vc = kc.clone() if not quant else kc.view(torch.uint8).clone().view(E4)
+    e = [torch.full((blocks, page, K), 9, dtype=torch.int8, device=DEV) if quant else None for _ in range(2)]
+    err = dev_error()
+    cuda_lib.spec_verify_append(k, -k, torch.tensor(slots, device=DEV), kc, vc, key_exps=e[0], value_exps=e[1],
+                                dev_error=err) if quant else \
+        cuda_lib.spec_verify_rope_append(None, k, -k, None, None, torch.tensor(slots, device=DEV), kc, vc, dev_error=err)
+    assert err.item() == cuda_lib.SV_DEVERR_PAGE
+    b, t = slots[on] // page, slots[on] % page
+    off = torch.ones(blocks, page, dtype=torch.bool, device=DEV)
+    off[torch.tensor(b, device=DEV), torch.tensor(t, device=DEV)] = False
+    for c, x, s in ((kc, e[0], 1.0), (vc, e[1], -1.0)):
+        assert bool((c.to(F32)[off] == 3).all()) and (x is None or bool((x[off] == 9).all()))
+        got, want = values(c, x)[b, t], s * np64(k)[on]
+        tol = 0 * want if not quant else np.maximum(
+            2.0 ** -4 * np.abs(want), 2.0 ** -10 * np.exp2(x.cpu().numpy().astype(np.float64))[b, t][..., None])
+        assert (np.abs(got - want) <= tol * (1 + 1e-9)).all()
+
+
+# ---------------------------------------------------------------- one stream of rows
+
+@pytest.mark.parametrize("codes,tree", [(True, False), (True, True), (False, True)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [1, 5, 8, 24, 64, 192])
+def test_pages_of_one_stream(cuda_lib, page, D, codes, tree):
+    """At most 128 rows an item, contexts of many turns of the ring, items that are cut."""
+    check_attention(cuda_lib, BF, codes, tree, [(5001, 16), (777, 9), (64, 1), (2600, 5), (16, 16)], 2, 5, D, page,
+                    layout="heads" if page % 2 else "tokens", seed=page)
+    check_attention(cuda_lib, BF, codes, tree, [(3000, 1), (9001, 1), (130, 1)], 1, 8, D, page, seed=page + 1)
+
+
+# ---------------------------------------------------------------- together
+
+def test_a_tree_step_s_attention_against_the_oracle(cuda_lib):
+    """Slots, masks, rotated queries and an 8-bit cache: what each row of the step's trees
+    attends to."""
+    st = tree_state(cuda_lib, 8)
+    n, B, K, G, D, new, ctx, par = st["nums"]
+    err = st["err"]
+    plan = cuda_lib.spec_verify_slots(st["ctx"], st["new"], st["table"], st["held"], st["free"], st["count"],
+                                      page_size=16, n_rows=st["rows"], dev_error=err)
+    pos, mask = cuda_lib.spec_verify_tree(st["parents"], plan.seq_lens, plan.row_offsets, max_len=64, dev_error=err)
+    offs = np.concatenate([[0], np.cumsum(new)])
+    for window in (0, 50):
+        q = cuda_lib.spec_verify_rope_append(st["q"][0], st["k"][0], st["v"][0], pos, st["freqs"], plan.slots,
+                                             st["kc"][0], st["vc"][0], key_exps=st["ke"][0], value_exps=st["ve"][0],
+                                             dev_error=err)
+        out, _ = cuda_lib.spec_verify_attention(q, st["kc"][0], st["vc"][0], st["table"], plan.seq_lens,
+                                                plan.row_offsets, max_len=64, key_exps=st["ke"][0],
+                                                value_exps=st["ve"][0], tree_mask=mask, positions=pos, window=window,
+                                                dev_error=err)
+        assert int(err) == 0
+        keys, vals = values(st["kc"][0], st["ke"][0]), values(st["vc"][0], st["ve"][0])
+        table, qn, o = st["table"].cpu().numpy(), np64(q), np64(out)
+        for r in range(B):
+            l, c = int(new[r]), int(ctx[r])
+            t = np.arange(c + l)
+            k, v = (x[table[r, t // 16], t % 16] for x in (keys, vals))
+            anc = T.ancestors([int(p) for p in par[offs[r]:offs[r + 1]]])
+            seen = np.zeros((l, c + l), bool)
+            for i in range(l):
+                seen[i, max(0, c + len(anc[i]) - window) if window else 0:c] = True
+                seen[i, [c + j for j in anc[i]]] = True
+            want, _, mag = T.attention(qn[offs[r]:offs[r + 1]], k, v, D ** -0.5, seen)
+            tol = 2.0 ** -7 * mag + np.repeat(2.0 ** -32 * np.abs(v).sum(0), G, 0) + 1e-30
+            assert (np.abs(o[offs[r]:offs[r + 1]] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("codes,tree", [(True, False), (True, True), (False, True)])
+@pytest.mark.parametrize("G,l,D", [(8, 1, 128), (4, 16, 128), (4, 64, 64)])
+def test_calls_repeat_bit_by_bit(cuda_lib, codes, tree, G, l, D):
+    """Whatever the workspace and the chip's memories held before."""
+    g, rng = torch.Generator(device=DEV).manual_seed(l), np.random.default_rng(l)
+    lens = [int(n) for n in rng.integers(l, 6000, 9)]
+    need = [-(-n // 16) for n in lens]
+    caches, exps = make_caches(g, rng, sum(need), 16, 2, D, BF, codes, "tokens")
+    table = np.zeros((9, max(need)), np.int64)
+    ids = np.split(rng.permutation(sum(need)), np.cumsum(need)[:-1])
+    for r in range(9):
+        table[r, :need[r]] = ids[r]
+    q = torch.randn(9 * l, 2 * G, D, device=DEV, generator=g).to(BF)
+    mask = pack([a for _ in range(9) for a in T.ancestors(random_tree(rng, l))], (l + 31) // 32) if tree else None
+    args = (*caches, i32(table), i32(lens), i32(np.arange(10) * l))
+    ws = cuda_lib.alloc_attention_workspace(q)
+    kw = dict(max_len=l, key_exps=exps[0], value_exps=exps[1], tree_mask=mask, want_lse=True, workspace=ws)
+    want = None
+    for i in range(12):
+        ws.copy_(torch.randint(0, 256, ws.shape, device=DEV, generator=g, dtype=torch.uint8) if i % 3 else
+                 torch.full_like(ws, 255))
+        if i % 2:  # operands of NaN and infinities stay behind
+            cuda_lib.spec_verify_attention(q * float("nan") if i % 4 == 1 else q * 1e38 * 10, *args, **{**kw, "workspace": None})
+        got = cuda_lib.spec_verify_attention(q, *args, **kw)
+        if want is None:
+            want = got
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
