@@ -8,8 +8,8 @@ import pytest
 import torch
 
 from oracle import tree_oracle as T
-from test_gpu_tree import (BF, DEV, E4, F32, check_attention, check_rope_append, close, dev_error, heads_of, i32,
-                           make_caches, np64, pack, random_tree, some_freqs, tree_state, values)
+from test_gpu_tree import (BF, DEV, E4, F32, check_attention, check_rope_append, close, copy_state, dev_error, heads_of,
+                           i32, make_caches, np64, pack, random_tree, some_freqs, tree_state, tree_step, values)
 
 pytestmark = pytest.mark.gpu
 
@@ -417,6 +417,28 @@ def test_a_tree_step_s_attention_against_the_oracle(cuda_lib):
             want, _, mag = T.attention(qn[offs[r]:offs[r + 1]], k, v, D ** -0.5, seen)
             tol = 2.0 ** -7 * mag + np.repeat(2.0 ** -32 * np.abs(v).sum(0), G, 0) + 1e-30
             assert (np.abs(o[offs[r]:offs[r + 1]] - want) <= tol).all()
+
+
+def test_a_tree_step_over_memory_in_any_state(cuda_lib):
+    """What the step's calls allocate may hold anything before; rows behind the last request
+    keep it."""
+    first = tree_state(cuda_lib, 11)
+    rows = int(first["nums"][5].sum())
+    stream, want = torch.cuda.Stream(), None
+    for i, x in enumerate((0.0, float("nan"), 3e38, float("nan"))):
+        st = copy_state(first)
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            for size in (1 << 10, 1 << 14, 1 << 18, 1 << 20, 1 << 22):
+                waste = [torch.full((size,), x, device=DEV) for _ in range(8)]
+                del waste
+        got = tree_step(cuda_lib, st, stream) if i != 1 else tree_step(cuda_lib, st)
+        torch.cuda.synchronize()
+        assert int(st["err"]) == 0
+        got = [y[:rows] for y in got[:2]] + got[2:]
+        want = want or [y.clone() for y in got]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("codes,tree", [(True, False), (True, True), (False, True)])
