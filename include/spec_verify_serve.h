@@ -277,7 +277,8 @@ int spec_verify_rope_append(const void* query, int64_t q_row_stride, int64_t q_h
  * but for rows far below the largest of their tile, the request's tokens 64 i .. 64 i + 63:
  * of rows whose exponent is more than 22 below the tile's largest (or below -102) up to
  * 2^-23 in units of 2^largest is lost.  Rows of the tile that a query does not see count
- * among them, and reach it in this way alone.
+ * among them, and reach it in this way alone.  Of a query's row and head, elements below
+ * 2^-31 of the largest may lose up to 2^-39 of it.
  */
 int spec_verify_attention_ext(
     const void* query, int64_t q_row_stride, int64_t q_head_stride, const void* key_cache,

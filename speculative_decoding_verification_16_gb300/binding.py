@@ -567,6 +567,7 @@ def spec_verify_attention(query, key_cache, value_cache, block_table, seq_lens, 
     ``window`` > 0 keeps the last window keys of each row; ``scale`` defaults to
     head_dim ** -0.5; ``max_len`` is a host upper bound of the new tokens of a
     request.  ``workspace`` (alloc_attention_workspace) is best kept between calls.
+    Rows behind the last request's are not written: of a new out they are undefined.
     Caches of float8_e4m3fn (bf16 queries) come with ``key_exps`` and ``value_exps``,
     int8 of the caches' shape without its last dimension.  ``tree_mask`` int32 [n_rows,
     words] (spec_verify_tree) makes the rows a tree's: each sees its request's context

@@ -118,9 +118,13 @@ int run_mma_from(const MmaArgs& p, const CUtensorMap& km, const CUtensorMap& vm,
                   : launch_mma<2, 128, SRC, TREE>(x, b.grid, b.items, b.joins, km, vm, st);
 }
 
-// What an item of this many rows costs beside its tiles, in tiles: 64 single tokens with 8
-// heads a group 428 us at 2, 418 at 6, 423 at 9; 32 trees of up to 64 tokens 148, 130, 125;
-// 32 x 16 tokens over a cache of 8 bits 196, 168, 161.
+// What an item of this many rows costs beside its tiles, in tiles.  32 requests over 512 to
+// 32,768 (trees 16,384) tokens, us at 2 / 4 / 6 / 8 / 10 / 12, codes of 8 rows an item 137 /
+// 131 / 133 / 134 / 135 / 139, 32 rows 153 / 143 / 135 / 135 / 136 / 139, 64 rows 164 / 150 /
+// 143 / 142 / 142 / 146, 128 rows 192 / 181 / 172 / 169 / 170 / 172, 256 rows in two streams
+// 335 / 305 / 279 / 266 / 255 / 253; bf16 trees of up to 32 rows 91 / 91 / 92 / 92 / 93 / 94,
+// 128 rows 103 / 101 / 101 / 102 / 103 / 104, 256 rows 145 / 131 / 126 / 122 / 124 / 127.  So
+// few rows want 4 to 6, many 8 to 12; about 64 rows either will do.
 int item_cost(int64_t rows) { return rows > 32 ? 10 : 6; }
 
 // E4M3: the caches hold codes and exponents; TREE: rows see what their masks name.

@@ -41,8 +41,8 @@
 // Caches of 8 bits: codes come by the same copies, and warps of their own turn them into
 // fp16 operands in place (turn_codes, below), so queries and weights are fp16 there too.
 // Decoding is bound by those warps and by shared memory, not by the half as many bytes:
-// 64 single tokens, 64/8 heads of 128, 2,048 to 32,768 cached, 395 us (3.9 TB/s, 0.57 of
-// the copy rate); 32 x 16 tokens 153 us; 3 chunks of 2,048 749 us (1.04 PFLOP/s), where
+// 64 single tokens, 64/8 heads of 128, 2,048 to 32,768 cached, 397 us (3.9 TB/s, 0.57 of
+// the copy rate); 32 x 16 tokens 153 us; 3 chunks of 2,048 760 us (1.02 PFLOP/s), where
 // the softmax and the codes share the issue slots.  The kernel's hot loops barely fit the
 // instruction cache: unrolling one of them moved the chunks by up to a third.
 //

@@ -408,7 +408,10 @@ template <typename T, bool QUANT, bool PAIRS>
 int launch_rope(const RopeArgs& args, bool wide, int sms, cudaStream_t st) {
   RopeArgs a = args;
   constexpr int kWarps = kRopeThreads / 32;
-  // rows for eight warps of every SM
+  // rows for eight warps of every SM.  At 608 / 1,216 / 2,432 rows a warp a row and a group a
+  // vector take, of 32/8 heads of 128 into 8 bits, 7.7 and 6.5 / 8.0 and 11.2 / 9.8 and 20.3
+  // us; of 16/4 heads of 80 into bf16 5.3 and 3.7 / 5.3 and 5.7 / 6.0 and 9.5; of 8/1 heads
+  // of 64 3.5 and 3.0 / 3.5 and 3.3 / 3.8 and 4.0
   if (wide && a.n_rows >= kWarps * sms)
     return launch(rope_row_kernel<T, QUANT, PAIRS>, dim3((a.n_rows + kWarps - 1) / kWarps), kRopeThreads,
                   kWarps * padded_pairs(a.half) * static_cast<int>(sizeof(float2)), 1, false, st, a);
