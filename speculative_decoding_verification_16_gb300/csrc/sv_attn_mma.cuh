@@ -1152,7 +1152,8 @@ __global__ __launch_bounds__(attn_threads(NS, DP, SRC), attn_per_sm(NS, DP)) voi
             }
             float s0, s1;
             unpack2(add2(sum[0], sum[1]), &s0, &s1);
-            l += (s0 + s1) * ex2(shift - e);
+            // at most 2^113, but for a row that sees nothing of the tile: 0, not 0 times infinity
+            l += (s0 + s1) * ex2(fminf(shift - e, 126.0f));
           } else {
             // scores so large that the rounding of r c would neither cancel nor be the same
             // beside each tile's E: differences of products first, exact where they count; or

@@ -127,6 +127,24 @@ def test_codes_of_tiles_far_apart(cuda_lib, steps, D, G, tree):
         check_numbers(cuda_lib, E4, lens, q, keys, vals, page, D ** -0.5, window=100)
 
 
+@pytest.mark.parametrize("D,G,tree", [(64, 1, False), (128, 4, False), (128, 4, True), (256, 2, True)])
+def test_codes_of_tiles_far_apart_that_rows_do_not_see(cuda_lib, D, G, tree):
+    """Rows that see nothing of a tile whose values are far smaller, or larger, than those
+    that they see."""
+    rng = np.random.default_rng(D + G)
+    lens = [(70, 55), (130, 100), (200, 140), (65, 65)]
+    for pattern in ([105, -100], [-100, 105], [100, -90, 100, -90], [-90, 60, -90, 60]):
+        q = torch.tensor(rng.standard_normal((sum(l for _, l in lens), 2 * G, D)), device=DEV).to(BF)
+        keys, vals = [], []
+        for n, _ in lens:
+            keys.append((some_codes(rng, n, 2, D, most=2.0), np.zeros((n, 2), int)))
+            e = np.array([pattern[t // 64 % len(pattern)] for t in range(n)])
+            vals.append((some_codes(rng, n, 2, D), np.repeat(e[:, None], 2, 1)))
+        check_numbers(cuda_lib, E4, lens, q, keys, vals, 16, D ** -0.5, tree=tree)
+        if not tree:
+            check_numbers(cuda_lib, E4, lens, q, keys, vals, 16, D ** -0.5, window=20)
+
+
 # Scores 2^17 + d of one unit each, exact in every type and in 32 bits: q k is 2^8 2^9 and
 # a product of small whole numbers d.  Their differences are exact too, so weights are as
 # far off as at any scale.  Over 16- and 32-bit caches scores are scaled before they are
