@@ -388,7 +388,7 @@ constexpr float kLift = 7.0f;
 constexpr int kFactorMin = -87;  // least E: 2^D / l stays a normal number
 constexpr float kRaise = 60.0f;  // log2 of how far l's terms may exceed 1
 constexpr float kApart = 60.0f;
-constexpr float kLargeScore = 1024.0f;  // of |r c|, from where on r c - D + E is off by 2^-14
+constexpr float kLargeScore = 1024.0f;  // of |r c|, above which r c + D - E is off by more than 2^-14
 // E of a tile whose rows' largest exponent is `most`.
 __device__ __forceinline__ int tile_exponent(int most) { return max(most - 7, kFactorMin); }
 
